@@ -252,7 +252,7 @@ def _own(s, op):
     elif op == "resize":
         up = B.resize_pages(s["table"], s["lens"], s["new_lens"], s["ref"], c["page"], **kw)
     else:
-        up = B.compact_pages(s["table"], s["lens"], s["ref"], c["page"], **kw)
+        up = B.compact_pages(s["table"], s["ref"], **kw)
     B.copy_pages(s["caches"], up.moves, up.n_moves, status=up.status)
     if op == "fork":
         return up.block_table, up.seq_lens, up.ref_count, s["caches"]
