@@ -85,9 +85,12 @@ typedef enum { HPC_HND = 0, HPC_NHD = 1 } hpc_kv_layout;
 #define HPC_DEV_BAD_SEQLEN 0x1u /* seq_len < 0 or > max tokens; the request gets no tiles and a zero output */
 #define HPC_DEV_BAD_PAGE 0x2u   /* a block_table entry outside [0, num_pages); no load is issued for that page
                                    and its tokens are left out of the request's softmax */
-#define HPC_DEV_CAPACITY 0x4u   /* more work items than the plan can hold (cannot happen for a valid plan) */
+#define HPC_DEV_CAPACITY 0x4u   /* more work items than the plan can hold (cannot happen for a valid plan), or too
+                                   few free pages (hpc_pages_resize, hpc_pages_fork) */
 #define HPC_DEV_TIMEOUT 0x8u    /* a bounded pipeline wait expired; the kernel gave up and returned */
-#define HPC_DEV_BAD_INDEX 0x10u /* a row index outside its table (hpc_gather_rows, hpc_merge_lse_gather) */
+#define HPC_DEV_BAD_INDEX 0x10u /* a row index outside its table (hpc_gather_rows, hpc_merge_lse_gather,
+                                   hpc_pages_fork), or a token id outside the vocabulary (hpc_verify_drafts) */
+#define HPC_DEV_BAD_PROBS 0x20u /* a row of probabilities without any mass (hpc_verify_drafts) */
 
 /* One unit of a CTA's work: tiles [tile_begin, tile_end) of one (request, kv head). */
 typedef struct {
@@ -473,6 +476,116 @@ HPC_API int hpc_decode_prologue(const void* qkv, const float* q_norm_w, const fl
                         const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
                         int32_t batch, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
                         uint32_t* status, void* stream);
+
+/* ---- prompts --------------------------------------------------------------------------
+ * The prompts of a batch are packed: the tokens of request r are rows [cu_seqlens[r], cu_seqlens[r+1])
+ * of q / k / v, with cu_seqlens int32 [batch + 1] ascending on the device. Rows past cu_seqlens[batch]
+ * (a padded batch) and before cu_seqlens[0] are neither read into a result nor written. */
+
+/* hpc_decode_prologue for every token of packed prompts (or of chunks of prompts): RMSNorm + RoPE
+ * on q and k, and the write of k and v into the cache. The new tokens of request r are the last
+ * n_r = cu_seqlens[r+1] - cu_seqlens[r] of its seq_lens[r] cached tokens: token i of them sits at
+ * position seq_lens[r] - n_r + i. ("vLLM x HPC-Ops" summary names the fused prologue for the decode
+ * step; this is the same arithmetic for the tokens that a prompt brings.)
+ *   qkv:    device bf16 [tokens][num_heads + 2*kv_heads][head_dim], 16-byte aligned.
+ *   q_out:  device bf16 [tokens][num_heads][head_dim].
+ *   k_out:  device bf16 [tokens][kv_heads][head_dim]: the normalised and rotated k, for
+ *           hpc_prompt_attention; or NULL.
+ *   Caches, scales, block_table, seq_lens, norms, eps, rope_theta as hpc_decode_prologue; the caches,
+ *   q_out and k_out 16-byte aligned. tokens <= INT32_MAX.
+ * seq_lens[r] < n_r, a length beyond the block table or a cu_seqlens that descends sets
+ * HPC_DEV_BAD_SEQLEN, writes no page and zeroes the q_out (and k_out) rows of those tokens; a page id
+ * out of range sets HPC_DEV_BAD_PAGE and skips that write. Two requests that write the same slot
+ * race for it. */
+HPC_API int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_t* cu_seqlens, int32_t batch,
+                                const float* q_norm_w, const float* k_norm_w, float eps, float rope_theta, void* q_out,
+                                void* k_out, void* k_pages, void* v_pages, hpc_dtype kv_dtype, hpc_kv_layout kv_layout,
+                                const float* k_scale, const float* v_scale, int32_t num_pages, int32_t page_size,
+                                const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
+                                int32_t num_heads, int32_t kv_heads, int32_t head_dim, uint32_t* status, void* stream);
+
+/* ---- verification of drafted tokens -----------------------------------------------------
+ * After hpc_decode_step_multi has run the target over the drafted tokens: which of them stand, and the
+ * token that follows. With p_t the target's and q_t the draft's probabilities at step t of request r,
+ * drafted token x_t is kept when uniforms[r][t] * q_t(x_t) < p_t(x_t). At the first that is not, one is
+ * drawn from max(p_t - q_t, 0) (from p_t where that has no mass); when all draft_lens[r] are kept, one is
+ * drawn from the next row of p. The draw is the lowest i with sum_{j <= i} w_j > uniforms[r][max_drafts] *
+ * sum_j w_j. Products, differences and sums in fp64. Probabilities need not sum to one; a value that
+ * is not positive and finite counts as zero.
+ *   draft_tokens: device int32 [batch][max_drafts].
+ *   target_probs: device [batch][max_drafts + 1][vocab], FP32 or BF16 (prob_dtype); target_stride is the
+ *                 distance of two rows in elements, >= vocab.
+ *   draft_probs:  device [batch][max_drafts][vocab], same type, rows draft_stride apart; or NULL: the
+ *                 draft is certain of its tokens (q_t = 1 at x_t).
+ *   uniforms:     device float [batch][max_drafts + 1], in [0, 1).
+ *   draft_lens:   device int32 [batch], tokens drafted for each request (0 .. max_drafts), or NULL: all
+ *                 max_drafts. Outside that range it is clamped and sets HPC_DEV_BAD_SEQLEN.
+ *   out_tokens:   device int32 [batch][max_drafts + 1]: the kept tokens, the drawn one, then -1.
+ *   accepted:     device int32 [batch], the number kept.
+ *   new_lens:     device int32 [batch] or NULL: seq_lens[r] - draft_lens[r] + accepted[r], the cached
+ *                 tokens that stand, for hpc_pages_resize.
+ *   max_drafts: 0 .. 256.
+ * A drafted id outside the vocabulary is rejected and sets HPC_DEV_BAD_INDEX. A row without mass gives
+ * -1 and sets HPC_DEV_BAD_PROBS. */
+HPC_API int hpc_verify_drafts(const int32_t* draft_tokens, const void* target_probs, int64_t target_stride,
+                              const void* draft_probs, int64_t draft_stride, hpc_dtype prob_dtype,
+                              const float* uniforms, const int32_t* draft_lens, const int32_t* seq_lens, int32_t batch,
+                              int32_t max_drafts, int32_t vocab, int32_t* out_tokens, int32_t* accepted,
+                              int32_t* new_lens, uint32_t* status, void* stream);
+
+/* ---- upkeep of the cache's pages ---------------------------------------------------------
+ * The state is the block table, the lengths and ref_count int32 [num_pages]: how many table entries (and
+ * other holders of the caller's own) hold each page, 0 when it is free. A request of n tokens holds the
+ * first ceil(n / page_size) entries of its row. The calls take the lowest free pages, in request order
+ * (and column order within a request), so their results do not depend on timing. They run on the device
+ * without a host sync, and list the pages whose data has to move as pairs (source, destination) for
+ * hpc_pages_copy, which is called once for all caches that share the table (the K and V of every layer),
+ * before anything reads or writes the destinations.
+ *   moves: device int32 [move_capacity][2], 8-byte aligned. n_moves: device int32.
+ * ref_in and ref_out may be one buffer, and so may table_in and table_out except in hpc_pages_fork;
+ * otherwise they must not overlap. Entries past what a request holds come back as -1.
+ * When there are too few free pages the call sets HPC_DEV_CAPACITY and n_moves 0 and changes nothing
+ * (outputs equal inputs; the forked table is all -1 with lengths 0). */
+
+/* Requests change from old_lens to new_lens tokens: pages past the new length are released (a page
+ * whose count falls to 0 is free at once, for this call too), and a request that grows takes pages for
+ * its new columns. A request that grows inside a part-filled page that others hold too (a count above 1
+ * after the releases) takes a copy of it first. new_lens 0 ends a request. A length below 0 or beyond
+ * the table sets HPC_DEV_BAD_SEQLEN and leaves the row as it is; a held entry outside the pool sets
+ * HPC_DEV_BAD_PAGE. move_capacity >= batch; batch <= 8192. */
+HPC_API int hpc_pages_resize(const int32_t* table_in, int32_t* table_out, int32_t batch, int32_t max_pages_per_req,
+                             int32_t page_size, const int32_t* old_lens, const int32_t* new_lens,
+                             const int32_t* ref_in, int32_t* ref_out, int32_t num_pages, int32_t* moves,
+                             int32_t move_capacity, int32_t* n_moves, uint32_t* status, void* stream);
+
+/* New row r is old row parents[r] (-1: an empty row): beams that are reordered, several samples of one
+ * prompt, requests that leave a batch. Full pages are shared. Of a part-filled last page the first
+ * child (lowest r) keeps the page and every other takes a copy. Rows that no child names are released.
+ * A parent outside [-1, rows_in) sets HPC_DEV_BAD_INDEX and gives an empty row; a parent with an
+ * invalid length sets HPC_DEV_BAD_SEQLEN and gives an empty row. move_capacity >= rows_out; rows <= 8192. */
+HPC_API int hpc_pages_fork(const int32_t* table_in, const int32_t* lens_in, int32_t rows_in, const int32_t* parents,
+                           int32_t* table_out, int32_t* lens_out, int32_t rows_out, int32_t max_pages_per_req,
+                           int32_t page_size, const int32_t* ref_in, int32_t* ref_out, int32_t num_pages,
+                           int32_t* moves, int32_t move_capacity, int32_t* n_moves, uint32_t* status, void* stream);
+
+/* Moves the n pages in use to ids 0 .. n - 1: the i-th page in use at or past n goes to the i-th free
+ * page below n; the others stay. Every table entry is renamed (one that names a free page or none
+ * becomes -1; one past the pool also sets HPC_DEV_BAD_PAGE). page_map: device int32 [num_pages], the new
+ * id of every page (-1: free), for holders outside the table. move_capacity >= num_pages / 2. */
+HPC_API int hpc_pages_compact(const int32_t* table_in, int32_t* table_out, int32_t batch, int32_t max_pages_per_req,
+                              const int32_t* ref_in, int32_t* ref_out, int32_t num_pages, int32_t* page_map,
+                              int32_t* moves, int32_t move_capacity, int32_t* n_moves, uint32_t* status, void* stream);
+
+/* Copies page moves[i][0] to page moves[i][1] in every cache, for i < *n_moves (read on the device).
+ *   caches: HOST array of n_caches device pointers, each [num_pages][page_bytes], 16-byte aligned;
+ *           page_bytes a multiple of 16. The pointers are copied at the call.
+ * The pairs run in no order: a page that is a destination twice, or a destination and a source, ends
+ * up with unspecified contents (the calls above never list one). An id outside the pool skips the
+ * pair and sets HPC_DEV_BAD_PAGE; *n_moves outside [0, move_capacity] is clamped and sets
+ * HPC_DEV_CAPACITY. */
+HPC_API int hpc_pages_copy(void* const* caches, int32_t n_caches, int64_t page_bytes, int32_t num_pages,
+                           const int32_t* moves, int32_t move_capacity, const int32_t* n_moves, uint32_t* status,
+                           void* stream);
 
 /* ---- decode step without caller scratch ------------------------------------------------ */
 

@@ -21,7 +21,8 @@ HPC_OK, HPC_ERR_ARG, HPC_ERR_SHAPE, HPC_ERR_DTYPE, HPC_ERR_ALIGN, HPC_ERR_CUDA, 
 HPC_BF16, HPC_FP32, HPC_E4M3 = 0, 1, 2
 HPC_HND, HPC_NHD = 0, 1
 _LAYOUTS = {"HND": HPC_HND, "NHD": HPC_NHD}
-DEV_STATUS = {"bad_seqlen": 0x1, "bad_page": 0x2, "capacity": 0x4, "timeout": 0x8, "bad_index": 0x10}
+DEV_STATUS = {"bad_seqlen": 0x1, "bad_page": 0x2, "capacity": 0x4, "timeout": 0x8, "bad_index": 0x10,
+              "bad_probs": 0x20}
 ITEM_DTYPE = np.dtype([("req", "<i4"), ("kv_head", "<i2"), ("flags", "<i2"),
                        ("tile_begin", "<i4"), ("tile_end", "<i4")])
 ITEM_DIRECT, ITEM_SECOND_SLOT = 1, 2
@@ -39,7 +40,9 @@ EXPORTS = ("hpc_step_record_bytes", "hpc_build_flags", "hpc_plan_workspace_bytes
            "hpc_status_string", "hpc_last_error", "hpc_abi_version", "hpc_decode_step_noalloc",
            "hpc_decode_step", "hpc_decode_step_workspace_bytes", "hpc_decode_step_prologue",
            "hpc_decode_step_multi", "hpc_decode_step_multi_workspace_bytes", "hpc_decode_step_lse",
-           "hpc_merge_lse", "hpc_wait_selftest", "hpc_merge_lse_gather", "hpc_gather_rows", "hpc_gather_pages")
+           "hpc_merge_lse", "hpc_wait_selftest", "hpc_merge_lse_gather", "hpc_gather_rows", "hpc_gather_pages",
+           "hpc_prompt_prologue", "hpc_verify_drafts", "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact",
+           "hpc_pages_copy")
 
 
 class HpcError(RuntimeError):
@@ -112,6 +115,14 @@ def _load(path=LIB):
         "hpc_merge_lse_gather": (ctypes.c_int, [vp, vp, ctypes.c_int64, vp, i32, i32, i32, i32, vp, vp, vp, vp]),
         "hpc_gather_rows": (ctypes.c_int, [vp, ctypes.c_int64, ctypes.c_int64, vp, ctypes.c_int64, vp, vp, vp]),
         "hpc_gather_pages": (ctypes.c_int, [vp, i32, i32, vp, vp, i32, i32, vp, vp, vp]),
+        "hpc_prompt_prologue": (ctypes.c_int, [vp, ctypes.c_int64, vp, i32, vp, vp, fp, fp, vp, vp, vp, vp, ctypes.c_int,
+                                               ctypes.c_int, vp, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp]),
+        "hpc_verify_drafts": (ctypes.c_int, [vp, vp, ctypes.c_int64, vp, ctypes.c_int64, ctypes.c_int, vp, vp, vp, i32,
+                                             i32, i32, vp, vp, vp, vp, vp]),
+        "hpc_pages_resize": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, vp, i32, vp, vp, vp]),
+        "hpc_pages_fork": (ctypes.c_int, [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp]),
+        "hpc_pages_compact": (ctypes.c_int, [vp, vp, i32, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp]),
+        "hpc_pages_copy": (ctypes.c_int, [ctypes.POINTER(vp), i32, ctypes.c_int64, i32, vp, i32, vp, vp, vp]),
         "hpc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hpc_last_error": (ctypes.c_char_p, []),
         "hpc_abi_version": (ctypes.c_int, []),
@@ -696,6 +707,247 @@ def gather_pages(block_table, req, col0, width=None, out=None, status=None):
         _check(_lib.hpc_gather_pages(_ptr(block_table), block_table.shape[0], block_table.shape[1], _ptr(req),
                                      _ptr(col0), n, width, _ptr(out), _ptr(status), _stream(dev)), "hpc_gather_pages")
     return out
+
+
+def _packed(cu_seqlens, dev, batch=None):
+    """Checks the boundaries of packed prompts; returns the number of requests."""
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    n = cu_seqlens.numel() - 1
+    if cu_seqlens.dim() != 1 or n < 1 or (batch is not None and n != batch):
+        raise HpcError("cu_seqlens must be [batch + 1]" + ("" if batch is None else f" for a batch of {batch}"))
+    return n
+
+
+def _status(status, dev):
+    if status is None:
+        return new_status(dev)
+    _need(status, "status", torch.int32, dev)
+    return status
+
+
+def _buffer(t, name, shape, dtype, dev):
+    """An output the caller may hand in."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise HpcError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block_table, seq_lens, num_heads, kv_heads,
+                    *, kv_dtype="bf16", kv_layout="HND", k_scale=None, v_scale=None, eps=1e-6, rope_theta=1e6,
+                    q_out=None, k_out=None, status=None):
+    """RMSNorm + RoPE + KV-page write of every token of packed prompts (``hpc_prompt_prologue``): qkv is
+    [tokens, Hq + 2 Hkv, D], request r's tokens are rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 and the
+    last of its seq_lens[r]. Returns (q_out [tokens, Hq, D], k_out [tokens, Hkv, D], status); rows of no
+    request are left as they were."""
+    _need(qkv, "qkv", torch.bfloat16)
+    dev = qkv.device
+    _need(q_norm_w, "q_norm_w", torch.float32, dev)
+    _need(k_norm_w, "k_norm_w", torch.float32, dev)
+    if qkv.dim() != 3 or qkv.shape[1] != num_heads + 2 * kv_heads:
+        raise HpcError("qkv must be [tokens, num_heads + 2*kv_heads, head_dim]")
+    n, _, D = qkv.shape
+    if q_norm_w.numel() != D or k_norm_w.numel() != D:
+        raise HpcError("norm weights must hold head_dim values")
+    code, num_pages, Hkv, P, lay = _cache(k_pages, v_pages, kv_dtype, kv_layout, k_scale, v_scale, D, dev)
+    if Hkv != kv_heads:
+        raise HpcError(f"cache has {Hkv} kv heads, expected {kv_heads}")
+    batch = _packed(cu_seqlens, dev)
+    _tables(block_table, seq_lens, batch, dev)
+    q_out = _buffer(q_out, "q_out", (n, num_heads, D), torch.bfloat16, dev)
+    k_out = _buffer(k_out, "k_out", (n, kv_heads, D), torch.bfloat16, dev)
+    status = _status(status, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_prompt_prologue(
+            _ptr(qkv), n, _ptr(cu_seqlens), batch, _ptr(q_norm_w), _ptr(k_norm_w), float(eps), float(rope_theta),
+            _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), code, lay, _ptr(k_scale), _ptr(v_scale), num_pages,
+            P, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), num_heads, kv_heads, D, _ptr(status),
+            _stream(dev)), "hpc_prompt_prologue")
+    return q_out, k_out, status
+
+
+def _rows(t, name, shape, dtype, dev):
+    """A [batch, steps, vocab] tensor whose rows are equally far apart; returns that distance."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != dev:
+        raise HpcError(f"{name} must be a CUDA tensor on {dev}")
+    if t.dtype != dtype:
+        raise HpcError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise HpcError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    Bn, T, V = shape
+    if V > 1 and t.stride(2) != 1:
+        raise HpcError(f"{name} must be contiguous along the vocabulary")
+    row = t.stride(1) if T > 1 else (t.stride(0) if Bn > 1 and T == 1 else V)
+    if (Bn > 1 and T > 0 and t.stride(0) != T * row) or row < V:
+        raise HpcError(f"{name} must have equally spaced rows")
+    return row
+
+
+def verify_drafts(draft_tokens, target_probs, draft_probs, uniforms, *, draft_lens=None, seq_lens=None,
+                  out_tokens=None, accepted=None, new_lens=None, status=None):
+    """Which drafted tokens stand, and the token after them (``hpc_verify_drafts``): draft_tokens int32
+    [B, T], target_probs [B, T + 1, V] and draft_probs [B, T, V] (or None: one-hot drafts) in fp32 or bf16,
+    uniforms fp32 [B, T + 1]. Rows may be padded (a view of a wider tensor). Returns (out_tokens [B, T + 1],
+    accepted [B], new_lens [B] or None, status); new_lens needs seq_lens."""
+    _need(draft_tokens, "draft_tokens", torch.int32)
+    dev = draft_tokens.device
+    if draft_tokens.dim() != 2 or not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 3:
+        raise HpcError("draft_tokens must be [batch, drafts] and target_probs [batch, drafts + 1, vocab]")
+    Bn, T = draft_tokens.shape
+    V = target_probs.shape[2]
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise HpcError(f"target_probs has dtype {target_probs.dtype}, expected float32 or bfloat16")
+    p_row = _rows(target_probs, "target_probs", (Bn, T + 1, V), target_probs.dtype, dev)
+    q_row = V
+    if draft_probs is not None:
+        q_row = _rows(draft_probs, "draft_probs", (Bn, T, V), target_probs.dtype, dev)
+    _need(uniforms, "uniforms", torch.float32, dev)
+    if tuple(uniforms.shape) != (Bn, T + 1):
+        raise HpcError(f"uniforms must be [{Bn}, {T + 1}]")
+    for name, t in (("draft_lens", draft_lens), ("seq_lens", seq_lens)):
+        if t is not None:
+            _need(t, name, torch.int32, dev)
+            if t.numel() != Bn:
+                raise HpcError(f"{name} must be [batch]")
+    out_tokens = _buffer(out_tokens, "out_tokens", (Bn, T + 1), torch.int32, dev)
+    accepted = _buffer(accepted, "accepted", (Bn,), torch.int32, dev)
+    if seq_lens is not None:
+        new_lens = _buffer(new_lens, "new_lens", (Bn,), torch.int32, dev)
+    elif new_lens is not None:
+        raise HpcError("new_lens needs seq_lens")
+    status = _status(status, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_verify_drafts(
+            _ptr(draft_tokens), _ptr(target_probs), p_row, _ptr(draft_probs), q_row,
+            HPC_FP32 if target_probs.dtype == torch.float32 else HPC_BF16, _ptr(uniforms), _ptr(draft_lens),
+            _ptr(seq_lens), Bn, T, V, _ptr(out_tokens), _ptr(accepted), _ptr(new_lens), _ptr(status), _stream(dev)),
+            "hpc_verify_drafts")
+    return out_tokens, accepted, new_lens, status
+
+
+@dataclass
+class PageUpdate:
+    """What ``resize_pages``, ``fork_pages`` or ``compact_pages`` leaves on the device. ``moves`` and
+    ``n_moves`` go to ``copy_pages``, before the destination pages are read or written."""
+
+    block_table: torch.Tensor
+    ref_count: torch.Tensor
+    moves: torch.Tensor  # int32 [capacity, 2], the first n_moves pairs (source, destination) valid
+    n_moves: torch.Tensor  # int32 [1]
+    status: torch.Tensor
+    seq_lens: torch.Tensor | None = None  # fork_pages
+    page_map: torch.Tensor | None = None  # compact_pages
+
+
+def _pool(block_table, ref_count):
+    """(device, rows, max_pages, num_pages) of a cache's table and reference counts."""
+    _need(block_table, "block_table", torch.int32)
+    dev = block_table.device
+    _need(ref_count, "ref_count", torch.int32, dev)
+    if block_table.dim() != 2 or ref_count.dim() != 1:
+        raise HpcError("block_table must be [rows, max_pages] and ref_count [num_pages]")
+    return dev, block_table.shape[0], block_table.shape[1], ref_count.numel()
+
+
+def _moves(moves, n_moves, capacity, dev):
+    if moves is None:
+        moves = torch.empty((max(capacity, 1), 2), dtype=torch.int32, device=dev)
+    _need(moves, "moves", torch.int32, dev)
+    if moves.dim() != 2 or moves.shape[1] != 2:
+        raise HpcError("moves must be [capacity, 2]")
+    return moves, _buffer(n_moves, "n_moves", (1,), torch.int32, dev)
+
+
+def resize_pages(block_table, old_lens, new_lens, ref_count, page_size, *, block_table_out=None, ref_count_out=None,
+                 moves=None, n_moves=None, status=None) -> PageUpdate:
+    """Requests change from old_lens to new_lens tokens (``hpc_pages_resize``): pages are released, taken,
+    and copied on write where a part-filled page is shared. Without output buffers the update is a new
+    table and new counts; handing the inputs in as outputs updates them in place."""
+    dev, Bn, M, N = _pool(block_table, ref_count)
+    for name, t in (("old_lens", old_lens), ("new_lens", new_lens)):
+        _need(t, name, torch.int32, dev)
+        if t.numel() != Bn:
+            raise HpcError(f"{name} must be [batch]")
+    table_out = _buffer(block_table_out, "block_table_out", (Bn, M), torch.int32, dev)
+    ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
+    moves, n_moves = _moves(moves, n_moves, Bn, dev)
+    status = _status(status, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_pages_resize(_ptr(block_table), _ptr(table_out), Bn, M, int(page_size), _ptr(old_lens),
+                                     _ptr(new_lens), _ptr(ref_count), _ptr(ref_out), N, _ptr(moves), moves.shape[0],
+                                     _ptr(n_moves), _ptr(status), _stream(dev)), "hpc_pages_resize")
+    return PageUpdate(table_out, ref_out, moves, n_moves, status)
+
+
+def fork_pages(block_table, seq_lens, ref_count, parents, page_size, *, block_table_out=None, seq_lens_out=None,
+               ref_count_out=None, moves=None, n_moves=None, status=None) -> PageUpdate:
+    """New row r is old row parents[r], -1 for none (``hpc_pages_fork``): full pages are shared, a
+    part-filled last page is copied for every child but the first, rows without children are released."""
+    dev, rows_in, M, N = _pool(block_table, ref_count)
+    _need(seq_lens, "seq_lens", torch.int32, dev)
+    if seq_lens.numel() != rows_in:
+        raise HpcError("seq_lens must be [rows]")
+    _need(parents, "parents", torch.int32, dev)
+    rows_out = parents.numel()
+    table_out = _buffer(block_table_out, "block_table_out", (rows_out, M), torch.int32, dev)
+    lens_out = _buffer(seq_lens_out, "seq_lens_out", (rows_out,), torch.int32, dev)
+    ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
+    moves, n_moves = _moves(moves, n_moves, rows_out, dev)
+    status = _status(status, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_pages_fork(_ptr(block_table), _ptr(seq_lens), rows_in, _ptr(parents), _ptr(table_out),
+                                   _ptr(lens_out), rows_out, M, int(page_size), _ptr(ref_count), _ptr(ref_out), N,
+                                   _ptr(moves), moves.shape[0], _ptr(n_moves), _ptr(status), _stream(dev)),
+               "hpc_pages_fork")
+    return PageUpdate(table_out, ref_out, moves, n_moves, status, seq_lens=lens_out)
+
+
+def compact_pages(block_table, ref_count, *, block_table_out=None, ref_count_out=None, page_map=None, moves=None,
+                  n_moves=None, status=None) -> PageUpdate:
+    """The pages in use move to the lowest ids (``hpc_pages_compact``); page_map names every page's new id."""
+    dev, Bn, M, N = _pool(block_table, ref_count)
+    table_out = _buffer(block_table_out, "block_table_out", (Bn, M), torch.int32, dev)
+    ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
+    page_map = _buffer(page_map, "page_map", (N,), torch.int32, dev)
+    moves, n_moves = _moves(moves, n_moves, N // 2, dev)
+    status = _status(status, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_pages_compact(_ptr(block_table), _ptr(table_out), Bn, M, _ptr(ref_count), _ptr(ref_out), N,
+                                      _ptr(page_map), _ptr(moves), moves.shape[0], _ptr(n_moves), _ptr(status),
+                                      _stream(dev)), "hpc_pages_compact")
+    return PageUpdate(table_out, ref_out, moves, n_moves, status, page_map=page_map)
+
+
+def copy_pages(caches, moves, n_moves, *, status=None):
+    """Copies the listed pages in every cache (``hpc_pages_copy``): caches is a list of tensors
+    [num_pages, ...] of one shape and element size, the K and V of every layer that shares the table.
+    Returns status."""
+    caches = list(caches)
+    _need(moves, "moves", torch.int32)
+    dev = moves.device
+    if moves.dim() != 2 or moves.shape[1] != 2:
+        raise HpcError("moves must be [capacity, 2]")
+    _need(n_moves, "n_moves", torch.int32, dev)
+    if n_moves.numel() != 1:
+        raise HpcError("n_moves must hold one count")
+    status = _status(status, dev)
+    if not caches:
+        return status
+    for t in caches:
+        _need(t, "cache", device=dev)
+        if t.dim() < 2 or t.shape != caches[0].shape or t.element_size() != caches[0].element_size():
+            raise HpcError("the caches must be [num_pages, ...] tensors of one shape and element size")
+    num_pages = caches[0].shape[0]
+    if num_pages == 0:
+        raise HpcError("the caches hold no pages")
+    page_bytes = caches[0][0].numel() * caches[0].element_size()
+    ptrs = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_pages_copy(ptrs, len(caches), page_bytes, num_pages, _ptr(moves), moves.shape[0],
+                                   _ptr(n_moves), _ptr(status), _stream(dev)), "hpc_pages_copy")
+    return status
 
 
 def wait_selftest(limit_ns: int, arrive: bool, device, status=None):

@@ -1,0 +1,642 @@
+// Upkeep of a paged KV cache on the device: resize (grow and free), fork, compact, and the copy of
+// the pages that those list.
+//
+// The state is a block table int32 [rows][max_pages], the lengths, and one reference count per
+// page (0 = free); there is no free list to keep in step. The pages taken are always the lowest
+// free ones, in request order, so a result depends on the inputs alone and not on which thread
+// came first (the counts change by integer atomics, whose order does not matter).
+//
+// Each planner is one launch of one cluster of 8 CTAs x 1024 threads. Its phases need a barrier over
+// all of the state (every release before the free pages are counted, every count before a page is
+// handed out); a cluster barrier costs a few hundred ns where another launch costs microseconds,
+// and the tables of a serving batch (64 K entries, 64 K pages) are a few hundred KB, which eight SMs
+// stream in a few microseconds. Free pages are found by a scan of the counts: each of the 256 warps
+// owns a contiguous run of pages, counts its free ones by ballot, and the warps' counts are prefixed
+// through distributed shared memory.
+//
+// The data is moved by pages_copy_kernel, for any number of caches (the K and V of every layer
+// share the table), from the list a planner leaves on the device. A destination was free and a
+// source is live, so no page is both.
+#include "hpc_common.cuh"
+
+namespace hpc {
+namespace {
+
+constexpr int kPgCtas = 8;        // one portable cluster
+constexpr int kPgThreads = 1024;  // per CTA
+constexpr int kPgWarps = kPgThreads / 32;
+constexpr int kPgAllWarps = kPgCtas * kPgWarps;
+constexpr int kPgMaxRows = 8192;  // rows whose needs fit in shared memory (12 bytes each at most)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// All threads of the cluster; orders their global and shared memory accesses. Not the .aligned forms: the
+// threads of a warp may come here from different branches.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Store to the same shared variable of CTA `rank` of the cluster.
+__device__ __forceinline__ void st_remote(uint32_t saddr, uint32_t rank, int32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Arrays that other CTAs of the cluster change: read past L1, and not moved over a barrier.
+__device__ __forceinline__ int32_t ld_shared_state(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ int2 ld_shared_state(const int2* p) {
+  int2 v;
+  asm volatile("ld.global.cg.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+
+
+// In place, s[0 .. n) -> exclusive prefix sums, returns the total (whole block).
+__device__ int32_t block_prefix(int32_t* s, int32_t n, int32_t* s_red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t base = 0;
+  __syncthreads();
+  for (int32_t i0 = 0; i0 < n; i0 += kPgThreads) {
+    const int32_t i = i0 + static_cast<int32_t>(threadIdx.x);
+    const int32_t v = i < n ? s[i] : 0;
+    int32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_red[warp] = x;
+    __syncthreads();
+    const int32_t w = s_red[lane];
+    const int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    if (i < n) s[i] = base + before + x - v;
+    base += __reduce_add_sync(0xffffffffu, w);
+  }
+  __syncthreads();
+  return base;
+}
+
+// Largest i with s[i] <= k, for an ascending prefix s[0 .. n) with s[0] = 0.
+__device__ __forceinline__ int32_t prefix_find(const int32_t* s, int32_t n, int32_t k) {
+  int32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (s[mid] <= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct PgShared {
+  int32_t red[kPgWarps];
+  int32_t a[kPgCtas], b[kPgCtas];  // per CTA of the cluster
+  int32_t wa[kPgWarps], wb[kPgWarps];
+};
+
+// The run of pages [begin, end) of a warp: the pool in 256 contiguous runs.
+__device__ __forceinline__ void warp_run(int32_t num_pages, int32_t gw, int32_t& begin, int32_t& end) {
+  const int64_t per = (((static_cast<int64_t>(num_pages) + kPgAllWarps - 1) / kPgAllWarps) + 31) & ~int64_t(31);
+  const int64_t b = per * gw, e = b + per;
+  begin = static_cast<int32_t>(b < num_pages ? b : num_pages);
+  end = static_cast<int32_t>(e < num_pages ? e : num_pages);
+}
+
+// Count of the pages of [begin, end) that `want` holds for (whole warp).
+template <typename F>
+__device__ __forceinline__ int32_t warp_count(const int32_t* ref, int32_t begin, int32_t end, F want) {
+  const int lane = threadIdx.x & 31;
+  int32_t c = 0;
+#pragma unroll 4
+  for (int32_t p = begin + lane; p < end; p += 32) c += want(p, ld_shared_state(ref + p)) ? 1 : 0;
+  return __reduce_add_sync(0xffffffffu, c);
+}
+
+// Calls visit(page, rank) for the pages of [begin, end) that `want` holds for, ranks ascending from
+// `rank`, until `limit` (whole warp).
+template <typename F, typename V>
+__device__ __forceinline__ void warp_visit(const int32_t* ref, int32_t begin, int32_t end, int32_t rank, int32_t limit,
+                                           F want, V visit) {
+  const int lane = threadIdx.x & 31;
+  for (int32_t p0 = begin; p0 < end && rank < limit; p0 += 32) {
+    const int32_t p = p0 + lane;
+    const bool w = p < end && want(p, ld_shared_state(ref + p));
+    const uint32_t m = __ballot_sync(0xffffffffu, w);
+    const int32_t k = rank + __popc(m & ((1u << lane) - 1u));
+    if (w && k < limit) visit(p, k);
+    rank += __popc(m);
+  }
+}
+
+// Per-warp counts -> this warp's exclusive prefix over the cluster and the total. Every thread of
+// the cluster calls it, after a first cluster_sync (a CTA's shared memory may be written only once it
+// runs); cta[] is the array of the CTAs' sums and warps[] the CTA's warps' counts.
+__device__ void cluster_prefix(int32_t count, int32_t* cta, int32_t* warps, int32_t& before, int32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster_rank();
+  if (lane == 0) warps[warp] = count;
+  __syncthreads();
+  const int32_t mine = __reduce_add_sync(0xffffffffu, warps[lane]);
+  if (threadIdx.x < kPgCtas) st_remote(smem_u32(cta + rank), threadIdx.x, mine);
+  cluster_sync();
+  before = total = 0;
+  for (int c = 0; c < kPgCtas; ++c) {
+    total += cta[c];
+    if (c < static_cast<int>(rank)) before += cta[c];
+  }
+  before += __reduce_add_sync(0xffffffffu, lane < warp ? warps[lane] : 0);
+}
+
+__device__ __forceinline__ void copy_counts(const int32_t* in, int32_t* out, int32_t n, int32_t gtid) {
+  if (in == out) return;
+  constexpr int kAll = kPgCtas * kPgThreads;
+  if (((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
+    const int32_t n4 = n >> 2;
+#pragma unroll 4
+    for (int32_t i = gtid; i < n4; i += kAll)
+      reinterpret_cast<int4*>(out)[i] = reinterpret_cast<const int4*>(in)[i];
+    for (int32_t i = 4 * n4 + gtid; i < n; i += kAll) out[i] = in[i];
+  } else {
+    for (int32_t i = gtid; i < n; i += kAll) out[i] = in[i];
+  }
+}
+
+struct PgArgs {
+  const int32_t* table_in;
+  int32_t* table_out;
+  const int32_t* lens;      // lengths of the rows of table_in
+  const int32_t* want;      // resize: new lengths; fork: parents
+  int32_t* lens_out;        // fork
+  const int32_t* ref_in;
+  int32_t* ref_out;
+  int32_t* page_map;        // compact
+  int2* moves;              // (source page, destination page)
+  int32_t* n_moves;
+  uint32_t* status;
+  int32_t rows_in, rows_out, max_pages, num_pages, page_size;
+};
+
+__device__ __forceinline__ bool len_ok(const PgArgs& a, int64_t n) {
+  return n >= 0 && n <= static_cast<int64_t>(a.max_pages) * a.page_size;
+}
+__device__ __forceinline__ int32_t held(const PgArgs& a, int64_t n) {
+  return static_cast<int32_t>((n + a.page_size - 1) / a.page_size);
+}
+
+// ---- resize -----------------------------------------------------------------------------
+// Row r goes from lens[r] to want[r] tokens. Pages past the new length are released (count - 1); a row
+// that grows takes pages for its new columns. A row that grows inside a part-filled page which
+// others still hold (count > 1 after the releases) first moves to a copy of it.
+__global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) pages_resize_kernel(const PgArgs a) {
+  extern __shared__ int32_t s_dyn[];
+  __shared__ PgShared sh;
+  int32_t* s_need = s_dyn;               // [rows] -> exclusive prefix
+  int32_t* s_cow = s_dyn + a.rows_out;   // [rows] 0 / 1 -> exclusive prefix
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int32_t gtid = static_cast<int32_t>(rank) * kPgThreads + static_cast<int32_t>(threadIdx.x);
+  const int32_t gw = gtid >> 5;
+  const int32_t M = a.max_pages, P = a.page_size, rows = a.rows_out;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  copy_counts(a.ref_in, a.ref_out, a.num_pages, gtid);
+  cluster_sync();
+  // releases; `sign` +1 takes them back
+  auto release = [&](int32_t sign) {
+    for (int32_t r = gw; r < rows; r += kPgAllWarps) {
+      const int64_t o = a.lens[r], n = a.want[r];
+      if (!len_ok(a, o) || !len_ok(a, n)) {
+        if (lane == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
+        continue;
+      }
+      for (int32_t j = held(a, n) + lane; j < held(a, o); j += 32) {
+        const int32_t p = a.table_in[static_cast<int64_t>(r) * M + j];
+        if (p >= 0 && p < a.num_pages) atomicAdd(a.ref_out + p, sign);
+        else atomicOr(a.status, HPC_DEV_BAD_PAGE);
+      }
+    }
+  };
+  release(-1);
+  cluster_sync();
+  // what every row needs, in every CTA
+  for (int32_t r = threadIdx.x; r < rows; r += kPgThreads) {
+    const int64_t o = a.lens[r], n = a.want[r];
+    int32_t need = 0, cow = 0;
+    if (len_ok(a, o) && len_ok(a, n) && n > o) {
+      need = held(a, n) - held(a, o);
+      if (o % P != 0) {
+        const int32_t p = a.table_in[static_cast<int64_t>(r) * M + o / P];
+        if (p < 0 || p >= a.num_pages) atomicOr(a.status, HPC_DEV_BAD_PAGE);
+        else if (ld_shared_state(a.ref_out + p) > 1) cow = 1;
+      }
+    }
+    s_need[r] = need + cow;
+    s_cow[r] = cow;
+  }
+  const int32_t total = block_prefix(s_need, rows, sh.red);
+  const int32_t copies = block_prefix(s_cow, rows, sh.red);
+  int32_t begin, end, before, free_pages;
+  warp_run(a.num_pages, gw, begin, end);
+  auto is_free = [](int32_t, int32_t c) { return c == 0; };
+  cluster_prefix(warp_count(a.ref_out, begin, end, is_free), sh.a, sh.wa, before, free_pages);
+  const bool fits = total <= free_pages;
+  if (gtid == 0) *a.n_moves = fits ? copies : 0;
+  if (!fits) {
+    // too few pages: the call changes nothing
+    if (gtid == 0) atomicOr(a.status, HPC_DEV_CAPACITY);
+    release(1);
+    if (a.table_in != a.table_out)
+      for (int64_t i = gtid; i < static_cast<int64_t>(rows) * M; i += kPgCtas * kPgThreads) a.table_out[i] = a.table_in[i];
+    return;
+  }
+  // the entries that stay, and -1 past them; the new ones are written below by whoever holds the page
+  for (int32_t r = gw; r < rows; r += kPgAllWarps) {
+    const int64_t o = a.lens[r], n = a.want[r];
+    const bool ok = len_ok(a, o) && len_ok(a, n);
+    const int32_t from = ok ? held(a, o) : M, to = ok ? held(a, n) : M;
+    const int32_t keep = from < to ? from : to;
+    const bool cow = (r + 1 < rows ? s_cow[r + 1] : copies) != s_cow[r];
+    const int32_t at = cow ? static_cast<int32_t>(o / P) : -1;
+    for (int32_t j = lane; j < M; j += 32) {
+      const int64_t i = static_cast<int64_t>(r) * M + j;
+      if (j < keep) {
+        if (j != at && a.table_in != a.table_out) a.table_out[i] = a.table_in[i];
+      } else if (j >= to) {
+        a.table_out[i] = -1;
+      }
+    }
+  }
+  warp_visit(a.ref_out, begin, end, before, total, is_free, [&](int32_t p, int32_t k) {
+    const int32_t r = prefix_find(s_need, rows, k);
+    const int64_t o = a.lens[r];
+    const bool cow = (r + 1 < rows ? s_cow[r + 1] : copies) != s_cow[r];
+    const int32_t nth = k - s_need[r];
+    const bool copy = cow && nth == 0;
+    const int32_t j = copy ? static_cast<int32_t>(o / P) : held(a, o) + nth - (cow ? 1 : 0);
+    const int64_t i = static_cast<int64_t>(r) * M + j;
+    if (copy) a.moves[s_cow[r]] = make_int2(a.table_in[i], p);
+    a.table_out[i] = p;
+    a.ref_out[p] = 1;
+  });
+  // The sources lose their sharer only once every warp has passed its free pages: a count that falls
+  // to zero here must not be taken in this call (its data is still to be copied).
+  if (copies > 0) {  // the same in every CTA
+    cluster_sync();
+    for (int32_t i = gtid; i < copies; i += kPgCtas * kPgThreads) {
+      const int2 mv = ld_shared_state(a.moves + i);
+      atomicAdd(a.ref_out + mv.x, -1);
+    }
+  }
+}
+
+// ---- fork -------------------------------------------------------------------------------
+// New row r is old row want[r] (-1: empty). A page that several rows come to hold is shared, except
+// a part-filled last page: the first child keeps it and every other takes a copy. Rows that no
+// child names are released with it.
+__global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) pages_fork_kernel(const PgArgs a) {
+  extern __shared__ int32_t s_dyn[];
+  __shared__ PgShared sh;
+  int32_t* s_need = s_dyn;                  // [rows_out] -> exclusive prefix
+  int32_t* s_kids = s_dyn + a.rows_out;     // [rows_in]
+  int32_t* s_first = s_kids + a.rows_in;    // [rows_in] first child
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int32_t gtid = static_cast<int32_t>(rank) * kPgThreads + static_cast<int32_t>(threadIdx.x);
+  const int32_t gw = gtid >> 5;
+  const int32_t M = a.max_pages, P = a.page_size, rows = a.rows_out;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  copy_counts(a.ref_in, a.ref_out, a.num_pages, gtid);
+  for (int32_t s = threadIdx.x; s < a.rows_in; s += kPgThreads) {
+    s_kids[s] = 0;
+    s_first[s] = rows;
+  }
+  __syncthreads();
+  for (int32_t r = threadIdx.x; r < rows; r += kPgThreads) {
+    const int32_t f = a.want[r];
+    if (f >= 0 && f < a.rows_in) {
+      atomicAdd(s_kids + f, 1);
+      atomicMin(s_first + f, r);
+    } else if (f != -1 && rank == 0) {
+      atomicOr(a.status, HPC_DEV_BAD_INDEX);
+    }
+  }
+  __syncthreads();
+  // length of new row r (0 for an empty row or a parent with an invalid length)
+  auto length = [&](int32_t r, int32_t& f) -> int64_t {
+    f = a.want[r];
+    if (f < 0 || f >= a.rows_in) return 0;
+    const int64_t n = a.lens[f];
+    return len_ok(a, n) ? n : 0;
+  };
+  for (int32_t r = threadIdx.x; r < rows; r += kPgThreads) {
+    int32_t f;
+    const int64_t n = length(r, f);
+    s_need[r] = n % P != 0 && s_first[f] != r ? 1 : 0;
+  }
+  const int32_t total = block_prefix(s_need, rows, sh.red);
+  cluster_sync();  // the counts are copied
+  // One change of count per held entry of an old row: its children less itself. Of a part-filled last
+  // page one child keeps the reference and the others leave.
+  auto recount = [&](int32_t sign) {
+    for (int32_t s = gw; s < a.rows_in; s += kPgAllWarps) {
+      const int64_t n = a.lens[s];
+      if (!len_ok(a, n)) {
+        if (lane == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
+        continue;
+      }
+      const int32_t kids = s_kids[s], np = held(a, n);
+      for (int32_t j = lane; j < np; j += 32) {
+        const int32_t p = a.table_in[static_cast<int64_t>(s) * M + j];
+        const bool part = j == np - 1 && n % P != 0;
+        const int32_t d = part ? (kids > 0 ? 0 : -1) : kids - 1;
+        if (p < 0 || p >= a.num_pages) atomicOr(a.status, HPC_DEV_BAD_PAGE);
+        else if (d != 0) atomicAdd(a.ref_out + p, sign * d);
+      }
+    }
+  };
+  recount(1);
+  cluster_sync();
+  int32_t begin, end, before, free_pages;
+  warp_run(a.num_pages, gw, begin, end);
+  auto is_free = [](int32_t, int32_t c) { return c == 0; };
+  cluster_prefix(warp_count(a.ref_out, begin, end, is_free), sh.a, sh.wa, before, free_pages);
+  const bool fits = total <= free_pages;
+  if (gtid == 0) {
+    *a.n_moves = fits ? total : 0;
+    if (!fits) atomicOr(a.status, HPC_DEV_CAPACITY);
+  }
+  if (!fits) recount(-1);  // too few pages: the counts as they were, and empty rows
+  for (int32_t r = gw; r < rows; r += kPgAllWarps) {
+    int32_t f;
+    const int64_t n = fits ? length(r, f) : 0;
+    if (lane == 0) a.lens_out[r] = static_cast<int32_t>(n);
+    const int32_t np = held(a, n);
+    const bool fresh = (r + 1 < rows ? s_need[r + 1] : total) != s_need[r];
+    for (int32_t j = lane; j < M; j += 32) {
+      if (j < np) {
+        if (!fresh || j != np - 1) a.table_out[static_cast<int64_t>(r) * M + j] = a.table_in[static_cast<int64_t>(f) * M + j];
+      } else {
+        a.table_out[static_cast<int64_t>(r) * M + j] = -1;
+      }
+    }
+  }
+  if (!fits) return;
+  warp_visit(a.ref_out, begin, end, before, total, is_free, [&](int32_t p, int32_t k) {
+    const int32_t r = prefix_find(s_need, rows, k);
+    int32_t f;
+    const int64_t n = length(r, f);
+    const int32_t j = static_cast<int32_t>(n / P);
+    a.moves[k] = make_int2(a.table_in[static_cast<int64_t>(f) * M + j], p);
+    a.table_out[static_cast<int64_t>(r) * M + j] = p;
+    a.ref_out[p] = 1;
+  });
+}
+
+// ---- compact ----------------------------------------------------------------------------
+// With n pages in use, the i-th used page at or past n goes to the i-th free page below n.
+__global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1) pages_compact_kernel(const PgArgs a) {
+  __shared__ PgShared sh;
+  __shared__ int32_t s_c[kPgCtas], s_w[kPgWarps];
+  const uint32_t rank = cluster_rank();
+  const int32_t gtid = static_cast<int32_t>(rank) * kPgThreads + static_cast<int32_t>(threadIdx.x);
+  const int32_t gw = gtid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t begin, end, unused, n, src0, srcs, dst0, dsts;
+  warp_run(a.num_pages, gw, begin, end);
+  cluster_sync();
+  cluster_prefix(warp_count(a.ref_in, begin, end, [](int32_t, int32_t c) { return c != 0; }), s_c, s_w, unused, n);
+  auto is_src = [n](int32_t p, int32_t c) { return c != 0 && p >= n; };
+  auto is_dst = [n](int32_t p, int32_t c) { return c == 0 && p < n; };
+  cluster_prefix(warp_count(a.ref_in, begin, end, is_src), sh.a, sh.wa, src0, srcs);
+  cluster_prefix(warp_count(a.ref_in, begin, end, is_dst), sh.b, sh.wb, dst0, dsts);
+  // srcs == dsts: the used pages below n and the sources make up n
+  warp_visit(a.ref_in, begin, end, src0, srcs, is_src, [&](int32_t p, int32_t k) { a.moves[k].x = p; });
+  warp_visit(a.ref_in, begin, end, dst0, dsts, is_dst, [&](int32_t p, int32_t k) { a.moves[k].y = p; });
+  for (int32_t p = begin + (threadIdx.x & 31); p < end; p += 32) {
+    const int32_t c = a.ref_in[p];
+    if (a.ref_in != a.ref_out) a.ref_out[p] = c;
+    a.page_map[p] = c != 0 ? p : -1;
+  }
+  if (gtid == 0) *a.n_moves = srcs;
+  cluster_sync();
+  for (int32_t k = gtid; k < srcs; k += kPgCtas * kPgThreads) {
+    const int2 mv = ld_shared_state(a.moves + k);
+    a.page_map[mv.x] = mv.y;
+    a.ref_out[mv.y] = ld_shared_state(a.ref_out + mv.x);
+    a.ref_out[mv.x] = 0;
+  }
+  cluster_sync();
+  const int64_t entries = static_cast<int64_t>(a.rows_in) * a.max_pages;
+#pragma unroll 4
+  for (int64_t i = gtid; i < entries; i += kPgCtas * kPgThreads) {
+    const int32_t p = a.table_in[i];
+    if (p >= a.num_pages) atomicOr(a.status, HPC_DEV_BAD_PAGE);
+    a.table_out[i] = p >= 0 && p < a.num_pages ? ld_shared_state(a.page_map + p) : -1;
+  }
+}
+
+// ---- copy -------------------------------------------------------------------------------
+constexpr int kPgCopyThreads = 256;
+constexpr int kPgCopyVecs = 4;  // 16-byte loads in flight per thread
+constexpr int kPgCopyChunk = kPgCopyThreads * kPgCopyVecs;
+constexpr int kPgMaxCaches = 256;  // pointers in one launch's parameters
+
+struct PgCaches {
+  uint4* base[kPgMaxCaches];
+};
+
+// Work is (move, cache, 16 KB chunk of the page), dealt over a persistent grid in that order.
+__global__ void __launch_bounds__(kPgCopyThreads)
+    pages_copy_kernel(const __grid_constant__ PgCaches caches, int32_t n_caches, int64_t page_vecs, int32_t num_pages,
+                      const int2* __restrict__ moves, const int32_t* __restrict__ n_moves, int32_t capacity,
+                      uint32_t* status) {
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t n = *n_moves;
+  if (n < 0 || n > capacity) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, HPC_DEV_CAPACITY);
+    n = n < 0 ? 0 : capacity;
+  }
+  const int64_t chunks = (page_vecs + kPgCopyChunk - 1) / kPgCopyChunk;
+  const int64_t per_move = chunks * n_caches;
+  for (int64_t w = blockIdx.x; w < per_move * n; w += gridDim.x) {
+    const int64_t m = w / per_move, rest = w - m * per_move;
+    const int64_t cache = rest / chunks, chunk = rest - cache * chunks;
+    const int2 mv = moves[m];
+    if (mv.x < 0 || mv.x >= num_pages || mv.y < 0 || mv.y >= num_pages) {
+      if (rest == 0 && threadIdx.x == 0) atomicOr(status, HPC_DEV_BAD_PAGE);
+      continue;
+    }
+    const uint4* src = caches.base[cache] + mv.x * page_vecs;
+    uint4* dst = caches.base[cache] + mv.y * page_vecs;
+    const int64_t i0 = chunk * kPgCopyChunk + threadIdx.x;
+    uint4 v[kPgCopyVecs];
+#pragma unroll
+    for (int k = 0; k < kPgCopyVecs; ++k)
+      if (i0 + k * kPgCopyThreads < page_vecs) v[k] = src[i0 + k * kPgCopyThreads];
+#pragma unroll
+    for (int k = 0; k < kPgCopyVecs; ++k)
+      if (i0 + k * kPgCopyThreads < page_vecs) dst[i0 + k * kPgCopyThreads] = v[k];
+  }
+}
+
+int check_common(const int32_t* table_in, const int32_t* table_out, const int32_t* ref_in, const int32_t* ref_out,
+                 int32_t rows_in, int32_t rows_out, int32_t max_pages, int32_t num_pages, const int32_t* moves,
+                 const int32_t* n_moves, const uint32_t* status) {
+  if (!table_in || !table_out || !ref_in || !ref_out || !moves || !n_moves || !status)
+    return fail(HPC_ERR_ARG, "null pointer argument");
+  if (rows_in < 1 || rows_out < 1 || max_pages < 1 || num_pages < 1) return fail(HPC_ERR_ARG, "sizes must be >= 1");
+  if (reinterpret_cast<uintptr_t>(moves) & 7u) return fail(HPC_ERR_ALIGN, "moves must be 8-byte aligned");
+  return HPC_OK;
+}
+
+int check_rows(int32_t rows, int32_t max_pages, int32_t page_size) {
+  if (rows > kPgMaxRows) return fail(HPC_ERR_SHAPE, "more than %d rows", kPgMaxRows);
+  if (page_size < 1) return fail(HPC_ERR_ARG, "page_size must be >= 1");
+  if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX)
+    return fail(HPC_ERR_SHAPE, "max_pages_per_req x page_size exceeds INT32_MAX");
+  return HPC_OK;
+}
+
+int launch_planner(void (*kernel)(PgArgs), const char* name, const PgArgs& args, size_t smem, void* stream) {
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return check_launch(name);
+  const cudaError_t e = launch_pdl(kernel, dim3(kPgCtas), dim3(kPgThreads), smem, static_cast<cudaStream_t>(stream), args);
+  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+  return check_launch(name);
+}
+
+}  // namespace
+}  // namespace hpc
+
+using namespace hpc;
+
+extern "C" int hpc_pages_resize(const int32_t* table_in, int32_t* table_out, int32_t batch, int32_t max_pages_per_req,
+                                int32_t page_size, const int32_t* old_lens, const int32_t* new_lens,
+                                const int32_t* ref_in, int32_t* ref_out, int32_t num_pages, int32_t* moves,
+                                int32_t move_capacity, int32_t* n_moves, uint32_t* status, void* stream) {
+  int rc = check_common(table_in, table_out, ref_in, ref_out, batch, batch, max_pages_per_req, num_pages, moves,
+                        n_moves, status);
+  if (rc != HPC_OK) return rc;
+  if (!old_lens || !new_lens) return fail(HPC_ERR_ARG, "null pointer argument");
+  if ((rc = check_rows(batch, max_pages_per_req, page_size)) != HPC_OK) return rc;
+  if (move_capacity < batch) return fail(HPC_ERR_CAPACITY, "moves must hold batch (%d) pairs", batch);
+  PgArgs a = {};
+  a.table_in = table_in;
+  a.table_out = table_out;
+  a.lens = old_lens;
+  a.want = new_lens;
+  a.ref_in = ref_in;
+  a.ref_out = ref_out;
+  a.moves = reinterpret_cast<int2*>(moves);
+  a.n_moves = n_moves;
+  a.status = status;
+  a.rows_in = a.rows_out = batch;
+  a.max_pages = max_pages_per_req;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  return launch_planner(pages_resize_kernel, "pages_resize_kernel", a, static_cast<size_t>(batch) * 8, stream);
+}
+
+extern "C" int hpc_pages_fork(const int32_t* table_in, const int32_t* lens_in, int32_t rows_in, const int32_t* parents,
+                              int32_t* table_out, int32_t* lens_out, int32_t rows_out, int32_t max_pages_per_req,
+                              int32_t page_size, const int32_t* ref_in, int32_t* ref_out, int32_t num_pages,
+                              int32_t* moves, int32_t move_capacity, int32_t* n_moves, uint32_t* status, void* stream) {
+  int rc = check_common(table_in, table_out, ref_in, ref_out, rows_in, rows_out, max_pages_per_req, num_pages, moves,
+                        n_moves, status);
+  if (rc != HPC_OK) return rc;
+  if (!lens_in || !lens_out || !parents) return fail(HPC_ERR_ARG, "null pointer argument");
+  if ((rc = check_rows(rows_in > rows_out ? rows_in : rows_out, max_pages_per_req, page_size)) != HPC_OK) return rc;
+  if (table_in == table_out || lens_in == lens_out)
+    return fail(HPC_ERR_ARG, "the forked table and lengths need buffers of their own");
+  if (move_capacity < rows_out) return fail(HPC_ERR_CAPACITY, "moves must hold rows_out (%d) pairs", rows_out);
+  PgArgs a = {};
+  a.table_in = table_in;
+  a.table_out = table_out;
+  a.lens = lens_in;
+  a.want = parents;
+  a.lens_out = lens_out;
+  a.ref_in = ref_in;
+  a.ref_out = ref_out;
+  a.moves = reinterpret_cast<int2*>(moves);
+  a.n_moves = n_moves;
+  a.status = status;
+  a.rows_in = rows_in;
+  a.rows_out = rows_out;
+  a.max_pages = max_pages_per_req;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  return launch_planner(pages_fork_kernel, "pages_fork_kernel", a,
+                        (static_cast<size_t>(rows_out) + 2 * static_cast<size_t>(rows_in)) * 4, stream);
+}
+
+extern "C" int hpc_pages_compact(const int32_t* table_in, int32_t* table_out, int32_t batch, int32_t max_pages_per_req,
+                                 const int32_t* ref_in, int32_t* ref_out, int32_t num_pages, int32_t* page_map,
+                                 int32_t* moves, int32_t move_capacity, int32_t* n_moves, uint32_t* status,
+                                 void* stream) {
+  const int rc = check_common(table_in, table_out, ref_in, ref_out, batch, batch, max_pages_per_req, num_pages, moves,
+                              n_moves, status);
+  if (rc != HPC_OK) return rc;
+  if (!page_map) return fail(HPC_ERR_ARG, "null pointer argument");
+  if (move_capacity < num_pages / 2)
+    return fail(HPC_ERR_CAPACITY, "moves must hold num_pages / 2 (%d) pairs", num_pages / 2);
+  PgArgs a = {};
+  a.table_in = table_in;
+  a.table_out = table_out;
+  a.ref_in = ref_in;
+  a.ref_out = ref_out;
+  a.page_map = page_map;
+  a.moves = reinterpret_cast<int2*>(moves);
+  a.n_moves = n_moves;
+  a.status = status;
+  a.rows_in = a.rows_out = batch;
+  a.max_pages = max_pages_per_req;
+  a.num_pages = num_pages;
+  return launch_planner(pages_compact_kernel, "pages_compact_kernel", a, 0, stream);
+}
+
+extern "C" int hpc_pages_copy(void* const* caches, int32_t n_caches, int64_t page_bytes, int32_t num_pages,
+                              const int32_t* moves, int32_t move_capacity, const int32_t* n_moves, uint32_t* status,
+                              void* stream) {
+  if (!caches || !moves || !n_moves || !status) return fail(HPC_ERR_ARG, "null pointer argument");
+  if (n_caches < 0 || page_bytes < 1 || num_pages < 1 || move_capacity < 0)
+    return fail(HPC_ERR_ARG, "sizes out of range");
+  if (page_bytes % 16) return fail(HPC_ERR_SHAPE, "page_bytes must be a multiple of 16");
+  if (reinterpret_cast<uintptr_t>(moves) & 7u) return fail(HPC_ERR_ALIGN, "moves must be 8-byte aligned");
+  for (int32_t i = 0; i < n_caches; ++i) {
+    if (!caches[i]) return fail(HPC_ERR_ARG, "null pointer argument");
+    if (!aligned16(caches[i])) return fail(HPC_ERR_ALIGN, "caches must be 16-byte aligned");
+  }
+  if (n_caches == 0 || move_capacity == 0) return HPC_OK;
+  const int64_t page_vecs = page_bytes / 16;
+  const int64_t chunks = (page_vecs + kPgCopyChunk - 1) / kPgCopyChunk;
+  const int sms = device_sm_count();
+  const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 148) * (2048 / kPgCopyThreads);
+  for (int32_t c0 = 0; c0 < n_caches; c0 += kPgMaxCaches) {
+    PgCaches list = {};
+    const int32_t nc = n_caches - c0 < kPgMaxCaches ? n_caches - c0 : kPgMaxCaches;
+    for (int32_t i = 0; i < nc; ++i) list.base[i] = static_cast<uint4*>(caches[c0 + i]);
+    const int64_t most = chunks * nc * move_capacity;  // the count itself is on the device
+    const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(most < resident ? most : resident)),
+                                     dim3(kPgCopyThreads), 0, static_cast<cudaStream_t>(stream), list, nc, page_vecs,
+                                     num_pages, reinterpret_cast<const int2*>(moves), n_moves, move_capacity, status);
+    if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "pages_copy_kernel: %s", cudaGetErrorString(e));
+    const int rc = check_launch("pages_copy_kernel");
+    if (rc != HPC_OK) return rc;
+  }
+  return HPC_OK;
+}

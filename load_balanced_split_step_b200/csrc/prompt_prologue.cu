@@ -1,0 +1,234 @@
+// Prompt prologue: QK-RMSNorm + RoPE on every token of a packed batch of prompts, and the write of
+// their K and V into the cache pages. The decode prologue (prologue.cu) for many tokens per request.
+//
+// y = x w / sqrt(mean x^2 + eps), then the NeoX rotation of the pairs (i, i + D/2) by pos theta^(-2i/D);
+// angles in fp64, because pos reaches 1e5. Token i of request r sits at position
+// seq_lens[r] - (cu[r+1] - cu[r]) + (i - cu[r]): the new tokens are the last of the request.
+//
+// Bound by memory: every head of a token is read once and written once or twice. A head is spread over
+// D/16 lanes: a lane holds 8 consecutive elements of each half, so that loads and stores are 16 bytes
+// wide, the rotation needs no exchange, and the mean square is reduced over D/16 lanes. A warp
+// therefore takes 512/D heads of one token at a time. It computes its token's D/2 angles itself (two per
+// lane) and never meets another warp. Where there are few tokens, the heads of one are split over
+// several warps, which each repeat the angles: up to about 8 warps per SM, latency is what counts.
+#include "hpc_common.cuh"
+
+namespace hpc {
+namespace {
+
+constexpr int kPpThreads = 128;
+constexpr int kPpWarps = kPpThreads / 32;
+
+struct PpArgs {
+  const __nv_bfloat16* qkv;
+  const int32_t* cu;
+  const int32_t* seq_lens;
+  const float* q_w;
+  const float* k_w;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  void* k_pages;
+  void* v_pages;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  uint32_t* status;
+  int64_t tokens, max_pages;
+  double theta;
+  float eps;
+  int32_t batch, Hq, Hkv, num_pages, P, nhd, fp8, parts;
+};
+
+// The request that token i belongs to: the last r with cu[r] <= i (whole warp, 32 probes a step).
+// cu[0] is 0 or less than i for every token it is asked about.
+__device__ __forceinline__ int32_t find_request(const int32_t* cu, int32_t batch, int64_t i) {
+  const int lane = threadIdx.x & 31;
+  int32_t lo = 0, n = batch;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int32_t step = (n + 31) >> 5;
+    const int32_t at = lo + lane * step;
+    const bool le = lane * step < n && cu[at] <= i;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const int32_t k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(w[k] << 16);
+    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPpThreads) prompt_prologue_kernel(const PpArgs a) {
+  constexpr int kLanes = D / 16;          // lanes per head
+  constexpr int kHeads = 32 / kLanes;     // heads per warp at a time
+  __shared__ __align__(16) float s_cos[kPpWarps][D / 2];
+  __shared__ __align__(16) float s_sin[kPpWarps][D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % kLanes, slot_head = lane / kLanes;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int64_t units = a.tokens * a.parts, stride = static_cast<int64_t>(gridDim.x) * kPpWarps;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPpWarps + warp; w < units; w += stride) {
+    const int64_t i = w / a.parts;
+    const int part = static_cast<int>(w - i * a.parts);
+    const int32_t first = a.cu[0], past = a.cu[a.batch];
+    if (i < first || i >= past) continue;  // no request's token: left as it is
+    const int32_t r = find_request(a.cu, a.batch, i);
+    const int64_t b = a.cu[r], e = a.cu[r + 1];
+    const int64_t L = a.seq_lens[r];
+    // what the lengths say has to hold together before anything is addressed by them
+    const bool ok = b <= i && i < e && L >= e - b && L <= a.max_pages * a.P;
+    const int64_t pos = ok ? L - (e - i) : 0;
+    const int32_t page = ok ? a.table[r * a.max_pages + pos / a.P] : -1;
+    const bool page_ok = ok && page >= 0 && page < a.num_pages;
+    if (part == 0 && lane == 0 && !page_ok) atomicOr(a.status, ok ? HPC_DEV_BAD_PAGE : HPC_DEV_BAD_SEQLEN);
+    __syncwarp();
+    for (int k = lane; k < D / 2; k += 32) {
+      double sn, cs;
+      sincos(static_cast<double>(pos) * pow(a.theta, -2.0 * k / D), &sn, &cs);
+      s_cos[warp][k] = static_cast<float>(cs);
+      s_sin[warp][k] = static_cast<float>(sn);
+    }
+    __syncwarp();
+    const int tok = static_cast<int>(pos % a.P);
+    const __nv_bfloat16* src = a.qkv + i * heads * D + 8 * sub;
+    const int groups = (heads + kHeads - 1) / kHeads;
+    const int g0 = groups * part / a.parts, g1 = groups * (part + 1) / a.parts;
+#pragma unroll 2
+    for (int g = g0; g < g1; ++g) {
+      const int h = g * kHeads + slot_head;
+      const bool live = h < heads;
+      uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
+      if (live) {
+        ra = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * D);
+        rb = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * D + D / 2);
+      }
+      float x[8], y[8];
+      unpack8(ra, x);
+      unpack8(rb, y);
+      float ss = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (!live) continue;
+      if (h < a.Hq + a.Hkv) {
+        const float inv = 1.f / sqrtf(ss / D + a.eps);
+        const float* wt = (h < a.Hq ? a.q_w : a.k_w) + 8 * sub;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float c = s_cos[warp][8 * sub + k], s = s_sin[warp][8 * sub + k];
+          const float p = x[k] * inv * wt[k], q = y[k] * inv * wt[D / 2 + k];
+          x[k] = p * c - q * s;
+          y[k] = q * c + p * s;
+        }
+      }
+      const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+      const int kv = is_q ? 0 : (is_k ? h - a.Hq : h - a.Hq - a.Hkv);
+      if (is_q || (is_k && a.k_out)) {
+        __nv_bfloat16* dst = (is_q ? a.q_out + (i * a.Hq + h) * D : a.k_out + (i * a.Hkv + kv) * D) + 8 * sub;
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst) = ok ? pack8(x) : z;
+        *reinterpret_cast<uint4*>(dst + D / 2) = ok ? pack8(y) : z;
+      }
+      if (is_q || !page_ok) continue;
+      const int64_t base = (a.nhd ? (static_cast<int64_t>(page) * a.P + tok) * a.Hkv + kv
+                                  : (static_cast<int64_t>(page) * a.Hkv + kv) * a.P + tok) * D + 8 * sub;
+      void* pages = is_k ? a.k_pages : a.v_pages;
+      if (a.fp8) {
+        const float sc = (is_k ? a.k_scale : a.v_scale)[kv];
+        uint8_t* dst = static_cast<uint8_t*>(pages) + base;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(f32x4_to_e4m3x4(x[0] / sc, x[1] / sc, x[2] / sc, x[3] / sc),
+                                                    f32x4_to_e4m3x4(x[4] / sc, x[5] / sc, x[6] / sc, x[7] / sc));
+        *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(f32x4_to_e4m3x4(y[0] / sc, y[1] / sc, y[2] / sc, y[3] / sc),
+                                                            f32x4_to_e4m3x4(y[4] / sc, y[5] / sc, y[6] / sc, y[7] / sc));
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + base;
+        *reinterpret_cast<uint4*>(dst) = pack8(x);
+        *reinterpret_cast<uint4*>(dst + D / 2) = pack8(y);
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace hpc
+
+using namespace hpc;
+
+extern "C" int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_t* cu_seqlens, int32_t batch,
+                                   const float* q_norm_w, const float* k_norm_w, float eps, float rope_theta,
+                                   void* q_out, void* k_out, void* k_pages, void* v_pages, hpc_dtype kv_dtype,
+                                   hpc_kv_layout kv_layout, const float* k_scale, const float* v_scale,
+                                   int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                                   int32_t max_pages_per_req, const int32_t* seq_lens, int32_t num_heads,
+                                   int32_t kv_heads, int32_t head_dim, uint32_t* status, void* stream) {
+  if (tokens < 0) return fail(HPC_ERR_ARG, "tokens must be >= 0");
+  if (tokens > INT32_MAX) return fail(HPC_ERR_SHAPE, "more tokens than int32 counts");
+  if (!cu_seqlens || !q_norm_w || !k_norm_w || !k_pages || !v_pages || !block_table || !seq_lens || !status ||
+      (tokens > 0 && (!qkv || !q_out)))
+    return fail(HPC_ERR_ARG, "null pointer argument");
+  if (kv_dtype != HPC_BF16 && kv_dtype != HPC_E4M3) return fail(HPC_ERR_DTYPE, "kv_dtype must be BF16 or E4M3");
+  if (kv_layout != HPC_HND && kv_layout != HPC_NHD) return fail(HPC_ERR_ARG, "kv_layout must be HND or NHD");
+  const bool fp8 = kv_dtype == HPC_E4M3;
+  if (fp8 && (!k_scale || !v_scale)) return fail(HPC_ERR_ARG, "E4M3 cache needs k_scale and v_scale");
+  if (batch < 1 || num_heads < 1 || kv_heads < 1 || num_pages < 1 || page_size < 1 || max_pages_per_req < 1)
+    return fail(HPC_ERR_ARG, "sizes must be >= 1");
+  if (num_heads % kv_heads) return fail(HPC_ERR_SHAPE, "num_heads %% kv_heads != 0");
+  if (head_dim != 64 && head_dim != 128) return fail(HPC_ERR_SHAPE, "head_dim must be 64 or 128");
+  if (!(rope_theta > 0.f) || !(eps >= 0.f)) return fail(HPC_ERR_ARG, "rope_theta must be > 0 and eps >= 0");
+  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(k_pages) || !aligned16(v_pages))
+    return fail(HPC_ERR_ALIGN, "qkv, q_out, k_out and the caches must be 16-byte aligned");
+  if (tokens == 0) return HPC_OK;
+  PpArgs a = {};
+  a.qkv = static_cast<const __nv_bfloat16*>(qkv);
+  a.cu = cu_seqlens;
+  a.seq_lens = seq_lens;
+  a.q_w = q_norm_w;
+  a.k_w = k_norm_w;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = block_table;
+  a.status = status;
+  a.tokens = tokens;
+  a.max_pages = max_pages_per_req;
+  a.theta = static_cast<double>(rope_theta);
+  a.eps = eps;
+  a.batch = batch;
+  a.Hq = num_heads;
+  a.Hkv = kv_heads;
+  a.num_pages = num_pages;
+  a.P = page_size;
+  a.nhd = kv_layout == HPC_NHD;
+  a.fp8 = fp8;
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  const int groups = (num_heads + 2 * kv_heads + 512 / head_dim - 1) / (512 / head_dim);
+  int64_t parts = (8 * static_cast<int64_t>(sms) + tokens - 1) / tokens;
+  if (parts > groups) parts = groups;
+  a.parts = static_cast<int32_t>(parts < 1 ? 1 : parts);
+  int64_t blocks = (tokens * a.parts + kPpWarps - 1) / kPpWarps;
+  const int64_t cap = static_cast<int64_t>(sms) * 8;
+  if (blocks > cap) blocks = cap;
+  auto kern = head_dim == 128 ? prompt_prologue_kernel<128> : prompt_prologue_kernel<64>;
+  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kPpThreads), 0,
+                                   static_cast<cudaStream_t>(stream), a);
+  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_prologue_kernel: %s", cudaGetErrorString(e));
+  return check_launch("prompt_prologue_kernel");
+}

@@ -1,0 +1,303 @@
+// Verification of drafted tokens against the target's probabilities (speculative decoding), from
+// given random numbers.
+//
+// With p_t the target's and q_t the draft's distribution at step t, drafted token x_t is kept when
+// u_t q_t(x_t) < p_t(x_t). At the first token that is not, one is drawn from the rest
+// max(p_t - q_t, 0) instead; when all are kept, one is drawn from p_T. The draw inverts the cumulative
+// sum: the lowest i with sum_{j <= i} w_j > u sum_j w_j. The result is distributed as the target's own
+// samples. Everything is compared and summed in fp64 (u q is exact there, and so is p - q for most
+// pairs of floats), so that the choice next to a border does not hang on the order of a sum.
+//
+// One cluster of CTAs per request. Each CTA decides the kept tokens on its own (a few words), so
+// that only the one row that is drawn from is read: 2 V values at a rejection, V otherwise, each once
+// from HBM. A warp owns a contiguous run of the vocabulary and sums it; the sums meet in distributed
+// shared memory; the one warp whose run holds the crossing reads its run again (from L2) to find it.
+#include "hpc_common.cuh"
+
+namespace hpc {
+namespace {
+
+constexpr int kVfThreads = 512;
+constexpr int kVfWarps = kVfThreads / 32;
+constexpr int kVfMaxCtas = 8;  // portable cluster
+constexpr int kVfMaxDrafts = 256;
+
+// Plain loads: an __ldg of a bf16 is an asm statement that the compiler may move ahead of the test
+// that guards it.
+__device__ __forceinline__ float vf_load(const float* p) { return *p; }
+__device__ __forceinline__ float vf_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// A probability: what is not a positive finite number counts as zero.
+__device__ __forceinline__ double vf_prob(float x) { return x > 0.f && x <= 3.402823466e38f ? static_cast<double>(x) : 0.0; }
+
+__device__ __forceinline__ double vf_warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct VfArgs {
+  const int32_t* drafts;
+  const void* p;
+  const void* q;
+  int64_t p_stride, q_stride;  // elements between rows (r, t)
+  const float* u;
+  const int32_t* draft_lens;
+  const int32_t* seq_lens;
+  int32_t* tokens;
+  int32_t* accepted;
+  int32_t* new_lens;
+  uint32_t* status;
+  int32_t T, V;
+};
+
+template <typename S>
+__global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int32_t ctas) {
+  __shared__ int32_t s_first;
+  __shared__ double s_warp[kVfWarps];
+  __shared__ double s_cta[2][kVfMaxCtas];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t r = blockIdx.x / ctas, rank = blockIdx.x % ctas;
+  const int32_t T = a.T, V = a.V;
+  // Shared memory of another CTA may be written only once that CTA runs: it says so here, and is
+  // waited for before the first such store.
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  pdl_wait();
+  pdl_launch_dependents();
+
+  int32_t n = T;
+  if (a.draft_lens) {
+    n = a.draft_lens[r];
+    if (n < 0 || n > T) {
+      if (rank == 0 && threadIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
+      n = n < 0 ? 0 : T;
+    }
+  }
+  if (threadIdx.x == 0) s_first = n;
+  __syncthreads();
+  const S* p_rows = static_cast<const S*>(a.p) + static_cast<int64_t>(r) * (T + 1) * a.p_stride;
+  const S* q_rows = a.q ? static_cast<const S*>(a.q) + static_cast<int64_t>(r) * T * a.q_stride : nullptr;
+  if (static_cast<int32_t>(threadIdx.x) < n) {
+    const int32_t t = threadIdx.x;
+    const int32_t x = a.drafts[static_cast<int64_t>(r) * T + t];
+    bool keep = false;
+    if (x < 0 || x >= V) {
+      if (rank == 0) atomicOr(a.status, HPC_DEV_BAD_INDEX);
+    } else {
+      const double px = vf_prob(vf_load(p_rows + t * a.p_stride + x));
+      const double qx = q_rows ? vf_prob(vf_load(q_rows + t * a.q_stride + x)) : 1.0;
+      keep = static_cast<double>(a.u[static_cast<int64_t>(r) * (T + 1) + t]) * qx < px;
+    }
+    if (!keep) atomicMin(&s_first, t);
+  }
+  __syncthreads();
+  const int32_t at = s_first;  // tokens kept; the step that is drawn
+  const bool cut = at < n;
+  const S* p = p_rows + at * a.p_stride;
+  bool rest = cut && q_rows;
+  const S* q = rest ? q_rows + at * a.q_stride : p;  // a valid row either way
+  int32_t gone = cut && !q_rows ? a.drafts[static_cast<int64_t>(r) * T + at] : -1;  // one-hot draft
+  const double u = static_cast<double>(a.u[static_cast<int64_t>(r) * (T + 1) + T]);
+
+  // this warp's run of the vocabulary
+  const int64_t per = (((static_cast<int64_t>(V) + ctas * kVfWarps - 1) / (ctas * kVfWarps)) + 31) & ~int64_t(31);
+  const int64_t b64 = per * (rank * kVfWarps + warp);
+  const int32_t begin = static_cast<int32_t>(b64 < V ? b64 : V);
+  const int32_t end = static_cast<int32_t>(b64 + per < V ? b64 + per : V);
+
+  auto weight = [&](int32_t i) -> double {
+    double w = vf_prob(vf_load(p + i));
+    if (rest) {
+      w -= vf_prob(vf_load(q + i));
+      w = w > 0.0 ? w : 0.0;
+    }
+    return i == gone ? 0.0 : w;
+  };
+  double total = 0.0, before = 0.0;
+  int used = 0;  // the round whose sums hold
+  for (int round = 0; round < 2; ++round) {
+    double sum = 0.0;
+    if (rest) {
+#pragma unroll 8
+      for (int32_t i = begin + lane; i < end; i += 32) {
+        const double w = vf_prob(vf_load(p + i)) - vf_prob(vf_load(q + i));
+        sum += w > 0.0 ? w : 0.0;
+      }
+    } else {
+#pragma unroll 8
+      for (int32_t i = begin + lane; i < end; i += 32) sum += i == gone ? 0.0 : vf_prob(vf_load(p + i));
+    }
+    sum = vf_warp_sum(sum);
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    if (static_cast<int32_t>(threadIdx.x) < ctas) {
+      double mine = 0.0;
+      for (int w = 0; w < kVfWarps; ++w) mine += s_warp[w];
+      uint32_t dst;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(&s_cta[round][rank])), "r"(threadIdx.x));
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dst), "d"(mine) : "memory");
+    }
+    // not the .aligned forms: nothing holds a warp together after the branch above
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    total = 0.0;
+    used = round;
+    for (int c = 0; c < ctas; ++c) {
+      if (c == rank) before = total;
+      total += s_cta[round][c];
+    }
+    if (total > 0.0 || (!rest && gone < 0)) break;  // the same in every CTA
+    // The rest has no mass (the target gives nothing outside the draft's share): the target's own row.
+    __syncthreads();
+    rest = false;
+    gone = -1;
+  }
+
+  int32_t* tokens = a.tokens + static_cast<int64_t>(r) * (T + 1);
+  if (rank == 0) {
+    for (int32_t t = threadIdx.x; t <= T; t += kVfThreads)
+      if (t < at) tokens[t] = a.drafts[static_cast<int64_t>(r) * T + t];
+      else if (t > at || !(total > 0.0)) tokens[t] = -1;
+    if (threadIdx.x == 0) {
+      a.accepted[r] = at;
+      if (a.new_lens) a.new_lens[r] = a.seq_lens[r] - n + at;
+      if (!(total > 0.0)) atomicOr(a.status, HPC_DEV_BAD_PROBS);
+    }
+  }
+  if (!(total > 0.0)) return;
+
+  // The CTA, then the warp, then the entry at which the running sum passes the target. Sums by part
+  // can round differently from the sums of the parts; where no part of the chosen one passes, the last with
+  // any mass is taken, which is the same entry up to that rounding. A u of 1 or more (or NaN)
+  // takes the last entry with mass.
+  const double target = u * total;
+  int chosen = -1, last = -1;
+  {
+    double run = 0.0;
+    for (int c = 0; c < ctas; ++c) {
+      const double s = s_cta[used][c];
+      run += s;
+      if (s > 0.0) last = c;
+      if (chosen < 0 && s > 0.0 && run > target) chosen = c;
+    }
+    if (chosen < 0) chosen = last;
+  }
+  if (chosen != rank) return;
+  int wsel = -1;
+  double base = before;
+  {
+    int wl = -1;
+    double run = before, bl = before;
+    for (int w = 0; w < kVfWarps; ++w) {
+      const double s = s_warp[w];
+      if (s > 0.0) {
+        if (wsel < 0 && run + s > target) {
+          wsel = w;
+          base = run;
+        }
+        wl = w;
+        bl = run;
+      }
+      run += s;
+    }
+    if (wsel < 0) {
+      wsel = wl;
+      base = bl;
+    }
+  }
+  if (warp != wsel) return;
+  // lanes own contiguous pieces of the run; then the piece, 32 entries at a time
+  const int32_t piece = static_cast<int32_t>(per >> 5);
+  double mine = 0.0;
+  {
+    const int64_t lo = static_cast<int64_t>(begin) + static_cast<int64_t>(lane) * piece;
+#pragma unroll 8
+    for (int32_t k = 0; k < piece; ++k)
+      if (lo + k < end) mine += weight(static_cast<int32_t>(lo + k));
+  }
+  auto inclusive = [&](double v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  const double inc = inclusive(mine);
+  const uint32_t mass = __ballot_sync(0xffffffffu, mine > 0.0);
+  uint32_t over = __ballot_sync(0xffffffffu, mine > 0.0 && base + inc > target);
+  const int lsel = over ? __ffs(over) - 1 : 31 - __clz(mass);
+  double run = base + (lsel > 0 ? __shfl_sync(0xffffffffu, inc, lsel - 1) : 0.0);
+  const int32_t lo = begin + lsel * piece;
+  const int32_t hi = lo + piece < end ? lo + piece : end;
+  int32_t found = -1, final_mass = -1;
+  for (int32_t i0 = lo; i0 < hi && found < 0; i0 += 32) {
+    const int32_t i = i0 + lane;
+    const double w = i < hi ? weight(i) : 0.0;
+    const double c = run + inclusive(w);
+    const uint32_t m = __ballot_sync(0xffffffffu, w > 0.0);
+    over = __ballot_sync(0xffffffffu, w > 0.0 && c > target);
+    if (over) found = i0 + __ffs(over) - 1;
+    if (m) final_mass = i0 + 31 - __clz(m);
+    run = __shfl_sync(0xffffffffu, c, 31);
+  }
+  if (lane == 0) tokens[at] = found >= 0 ? found : final_mass;
+}
+
+template <typename S>
+cudaError_t launch_verify(const VfArgs& a, int32_t batch, int32_t ctas, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch) * ctas);
+  cfg.blockDim = dim3(kVfThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<S>, a, ctas);
+}
+
+}  // namespace
+}  // namespace hpc
+
+using namespace hpc;
+
+extern "C" int hpc_verify_drafts(const int32_t* draft_tokens, const void* target_probs, int64_t target_stride,
+                                 const void* draft_probs, int64_t draft_stride, hpc_dtype prob_dtype,
+                                 const float* uniforms, const int32_t* draft_lens, const int32_t* seq_lens,
+                                 int32_t batch, int32_t max_drafts, int32_t vocab, int32_t* out_tokens,
+                                 int32_t* accepted, int32_t* new_lens, uint32_t* status, void* stream) {
+  if (!target_probs || !uniforms || !out_tokens || !accepted || !status || (max_drafts > 0 && !draft_tokens))
+    return fail(HPC_ERR_ARG, "null pointer argument");
+  if (new_lens && !seq_lens) return fail(HPC_ERR_ARG, "new_lens needs seq_lens");
+  if (prob_dtype != HPC_FP32 && prob_dtype != HPC_BF16) return fail(HPC_ERR_DTYPE, "probabilities must be FP32 or BF16");
+  if (batch < 1 || max_drafts < 0 || vocab < 1) return fail(HPC_ERR_ARG, "sizes out of range");
+  if (max_drafts > kVfMaxDrafts) return fail(HPC_ERR_SHAPE, "max_drafts above %d", kVfMaxDrafts);
+  if (batch > INT32_MAX / kVfMaxCtas) return fail(HPC_ERR_SHAPE, "batch too large");
+  if (target_stride < vocab || (draft_probs && draft_stride < vocab))
+    return fail(HPC_ERR_ARG, "a row stride is smaller than the vocabulary");
+  VfArgs a = {};
+  a.drafts = draft_tokens;
+  a.p = target_probs;
+  a.q = max_drafts > 0 ? draft_probs : nullptr;
+  a.p_stride = target_stride;
+  a.q_stride = draft_stride;
+  a.u = uniforms;
+  a.draft_lens = draft_lens;
+  a.seq_lens = seq_lens;
+  a.tokens = out_tokens;
+  a.accepted = accepted;
+  a.new_lens = new_lens;
+  a.status = status;
+  a.T = max_drafts;
+  a.V = vocab;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = prob_dtype == HPC_FP32 ? launch_verify<float>(a, batch, kVfMaxCtas, st)
+                                               : launch_verify<__nv_bfloat16>(a, batch, kVfMaxCtas, st);
+  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "verify_kernel: %s", cudaGetErrorString(e));
+  return check_launch("verify_kernel");
+}

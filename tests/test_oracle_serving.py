@@ -1,0 +1,159 @@
+"""Pins for oracle.pages, oracle.verify and oracle.prompt, and the host checks of the entry points they
+belong to (argument errors return codes before any CUDA call)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from load_balanced_split_step_b200 import build
+from oracle import pages as OP
+from oracle import prompt as OQ
+from oracle import verify as OV
+
+
+@pytest.fixture(scope="module")
+def B():
+    build.build()
+    from load_balanced_split_step_b200 import binding
+    return binding
+
+
+def test_pages_keep_the_counts_of_their_table():
+    rng = np.random.default_rng(0)
+    P, N, M = 4, 60, 6
+    table, lens = np.full((6, M), -1), np.zeros(6, dtype=int)
+    ref = np.zeros(N, dtype=int)
+    for step in range(60):
+        new = np.clip(lens + rng.integers(-6, 8, 6), 0, M * P)
+        got = OP.resize(table, lens, new, ref, P)
+        assert got is not None
+        table, ref, moves = got
+        lens = new
+        assert np.array_equal(ref, OP.counts(table, lens, N, P))
+        assert all((row >= 0).sum() == OP.held(n, P) for row, n in zip(table, lens))
+        # a part-filled last page that a row just grew in is its own
+        got = OP.fork(table, lens, ref, rng.integers(-1, 6, 6), P)
+        if got is None:
+            continue
+        table, lens, ref, moves = got
+        assert np.array_equal(ref, OP.counts(table, lens, N, P))
+        part = [row[OP.held(n, P) - 1] for row, n in zip(table, lens) if n % P]
+        assert len(set(part)) == len(part)
+        if step % 5 == 0:
+            table, ref, page_map, moves = OP.compact(table, ref)
+            n = int((ref > 0).sum())
+            assert (ref[:n] > 0).all() and not ref[n:].any()
+            assert np.array_equal(ref, OP.counts(table, lens, N, P))
+
+
+def test_pages_hold_what_was_written():
+    """Tokens written through the table are still there after forks, growth and compaction: a dict from
+    (page, slot) to token stands for the cache."""
+    rng = np.random.default_rng(1)
+    P, N, M = 4, 64, 5
+    cache = np.full((N, P), -1)
+    table, lens, ref = np.full((4, M), -1), np.zeros(4, dtype=int), np.zeros(N, dtype=int)
+    text = [[] for _ in range(4)]
+    for step in range(80):
+        new = np.clip(lens + rng.integers(-5, 6, 4), 0, M * P)
+        table, ref, moves = OP.resize(table, lens, new, ref, P)
+        for a, b in moves:
+            cache[b] = cache[a]
+        for r in range(4):
+            text[r] = text[r][:new[r]]
+            for pos in range(len(text[r]), new[r]):
+                text[r].append(step * 100 + r * 10 + pos)
+                cache[table[r, pos // P], pos % P] = text[r][-1]
+        lens = new
+        got = OP.fork(table, lens, ref, rng.integers(0, 4, 4), P)
+        if step % 3 == 0 and got is not None:
+            par = rng.integers(0, 4, 4)
+            table, lens, ref, moves = OP.fork(table, lens, ref, par, P)
+            text = [list(text[f]) for f in par]
+            for a, b in moves:
+                cache[b] = cache[a]
+        if step % 7 == 0:
+            table, ref, _, moves = OP.compact(table, ref)
+            for a, b in moves:
+                cache[b] = cache[a]
+        for r in range(4):
+            assert [int(cache[table[r, i // P], i % P]) for i in range(lens[r])] == text[r]
+
+
+def test_verify_follows_the_target():
+    """Exact for two tokens: P(first = 0) is the measure of the u that lead there, and equals p(0)."""
+    p, q = np.array([[0.7, 0.3], [0.5, 0.5]]), np.array([[0.2, 0.8]])
+    grid = (np.arange(200) + 0.5) / 200
+    mass = 0.0
+    for x, share in ((0, 0.2), (1, 0.8)):
+        hits = [OV.verify_one([x], p, q, [a, 0.5], 1)[0][0] == 0 for a in grid]
+        mass += share * np.mean(hits)  # the rest max(p - q, 0) is token 0 alone, whatever the last u
+    assert abs(mass - 0.7) <= 0.005
+    assert OV.sample(np.array([0.25, 0.0, 0.75]), 0.25) == 2 and OV.sample(np.array([0.25, 0.0, 0.75]), 0.0) == 0
+    assert OV.sample(np.zeros(3), 0.5) == -1
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_attention_against_sdpa(causal):
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((7, 4, 8), (12, 2, 8), (12, 2, 8)))
+    out, lse = OQ.attention(q, k, v, 0.3, causal)
+    mask = torch.ones(7, 12, dtype=torch.bool).tril(5) if causal else torch.ones(7, 12, dtype=torch.bool)
+    want = torch.nn.functional.scaled_dot_product_attention(
+        q.transpose(0, 1), k.transpose(0, 1).repeat_interleave(2, 0), v.transpose(0, 1).repeat_interleave(2, 0),
+        attn_mask=mask, scale=0.3).transpose(0, 1)
+    assert np.abs(out - want.numpy()).max() < 1e-12
+    s = torch.einsum("ihd,jhd->ihj", q, k.repeat_interleave(2, 1)) * 0.3
+    s = s.masked_fill(~mask[:, None], -torch.inf)
+    assert np.abs(lse - torch.logsumexp(s, -1).numpy()).max() < 1e-12
+    out, lse = OQ.attention(q, k[:3], v[:3], 0.3, True)  # more queries than keys: the first see none
+    assert not out[:4].any() and np.isinf(lse[:4]).all() and np.abs(out[4] - v[0].repeat_interleave(2, 0).numpy()).max() < 1e-12
+
+
+def test_host_checks_of_the_page_calls(B):
+    w, odd = ctypes.c_void_p(256), ctypes.c_void_p(260)
+    lib = B._lib
+
+    def resize(table=w, batch=2, pages=3, P=16, old=w, moves=w, cap=2, N=10):
+        return lib.hpc_pages_resize(table, w, batch, pages, P, old, w, w, w, N, moves, cap, w, w, None)
+
+    assert resize(table=None) == resize(old=None) == resize(moves=None) == B.HPC_ERR_ARG
+    assert resize(batch=0) == resize(pages=0) == resize(P=0) == resize(N=0) == B.HPC_ERR_ARG
+    assert resize(moves=odd) == B.HPC_ERR_ALIGN
+    assert resize(batch=8193, cap=9000) == B.HPC_ERR_SHAPE
+    assert resize(pages=1 << 20, P=1 << 12) == B.HPC_ERR_SHAPE
+    assert resize(cap=1) == B.HPC_ERR_CAPACITY
+
+    def fork(t_out=ctypes.c_void_p(512), l_out=ctypes.c_void_p(512), parents=w, rows=2, cap=2):
+        return lib.hpc_pages_fork(w, w, 2, parents, t_out, l_out, rows, 3, 16, w, w, 10, w, cap, w, w, None)
+
+    assert fork(parents=None) == B.HPC_ERR_ARG and fork(t_out=w) == B.HPC_ERR_ARG and fork(l_out=w) == B.HPC_ERR_ARG
+    assert fork(rows=0) == B.HPC_ERR_ARG and fork(cap=1) == B.HPC_ERR_CAPACITY
+    assert lib.hpc_pages_compact(w, w, 2, 3, w, w, 10, None, w, 5, w, w, None) == B.HPC_ERR_ARG
+    assert lib.hpc_pages_compact(w, w, 2, 3, w, w, 10, w, w, 4, w, w, None) == B.HPC_ERR_CAPACITY
+    ptrs = (ctypes.c_void_p * 2)(256, 264)
+    assert lib.hpc_pages_copy(None, 1, 16, 4, w, 1, w, w, None) == B.HPC_ERR_ARG
+    assert lib.hpc_pages_copy(ptrs, 1, 24, 4, w, 1, w, w, None) == B.HPC_ERR_SHAPE
+    assert lib.hpc_pages_copy(ptrs, 2, 32, 4, w, 1, w, w, None) == B.HPC_ERR_ALIGN
+    assert lib.hpc_pages_copy(ptrs, 1, 32, 4, w, 0, w, w, None) == B.HPC_OK  # nothing to do
+
+
+def test_host_checks_of_verify_and_prologue(B):
+    w = ctypes.c_void_p(256)
+    lib = B._lib
+
+    def verify(drafts=w, p=w, ps=100, q=w, qs=100, dt=B.HPC_FP32, seq=w, batch=2, T=3, V=100, new=w):
+        return lib.hpc_verify_drafts(drafts, p, ps, q, qs, dt, w, None, seq, batch, T, V, w, w, new, w, None)
+
+    assert verify(p=None) == verify(drafts=None) == verify(seq=None) == B.HPC_ERR_ARG
+    assert verify(ps=99) == verify(qs=99) == verify(batch=0) == verify(V=0) == verify(T=-1) == B.HPC_ERR_ARG
+    assert verify(dt=B.HPC_E4M3) == B.HPC_ERR_DTYPE and verify(T=257) == B.HPC_ERR_SHAPE
+
+    def pro(tokens=4, qkv=w, cu=w, kv=B.HPC_BF16, ks=None, D=64, heads=8, theta=1e6, q_out=w):
+        return lib.hpc_prompt_prologue(qkv, tokens, cu, 2, w, w, 1e-6, theta, q_out, None, w, w, kv, 0, ks, ks, 4, 16, w,
+                                       3, w, heads, 2, D, w, None)
+
+    assert pro(qkv=None) == pro(cu=None) == pro(tokens=-1) == pro(theta=0.0) == pro(kv=B.HPC_E4M3) == B.HPC_ERR_ARG
+    assert pro(kv=B.HPC_FP32) == B.HPC_ERR_DTYPE and pro(D=96) == pro(heads=7) == pro(tokens=1 << 31) == B.HPC_ERR_SHAPE
+    assert pro(q_out=ctypes.c_void_p(264)) == B.HPC_ERR_ALIGN and pro(tokens=0) == B.HPC_OK
