@@ -504,6 +504,44 @@ HPC_API int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_t* 
                                 const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
                                 int32_t num_heads, int32_t kv_heads, int32_t head_dim, uint32_t* status, void* stream);
 
+/* Attention of packed prompts: query i of sequence r (of n_r) sits at key position i + m_r - n_r of the
+ * sequence's m_r keys and, when causal != 0, sees the keys up to its own; otherwise all m_r.
+ *   out[i][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(sm_scale q[i][h] . k_j),  lse[i][h] = log sum_j p_j.
+ * (The pages report the attention backend's effect on time to first token ("vLLM x HPC-Ops" summary;
+ * remio.ai, "Por que Tencent HPC importa ...") but describe no prefill kernel.)
+ *   q, k, v: device bf16, head_dim contiguous, rows (token, head) at token_stride and head_stride
+ *            elements (multiples of 8; views into one packed qkv tensor will do), 16-byte aligned.
+ *   tokens, kv_tokens: rows of q and out, and of k and v.
+ *   cu_seqlens, cu_seqlens_k: the sequences' rows of q and of k / v. cu_seqlens_k NULL: as cu_seqlens
+ *            (kv_tokens must equal tokens).
+ *   out:     device bf16 [tokens][num_heads][head_dim].
+ *   lse:     device float [tokens][num_heads] or NULL.
+ *   head_dim 64 or 128; num_heads / kv_heads in {1, 2, 4, 8}; sm_scale positive and finite.
+ * A query that sees no key (m_r < n_r) gets zeros and -inf. A sequence whose lengths do not hold together
+ * (descending, or past tokens / kv_tokens) sets HPC_DEV_BAD_SEQLEN and is left out. Values of keys that a
+ * query does not see never reach its result, infinities and NaN included. P is rounded to bf16 for its
+ * product with V; sums and the softmax are fp32. */
+HPC_API int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                                 int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                 int64_t v_head_stride, int64_t tokens, int64_t kv_tokens, const int32_t* cu_seqlens,
+                                 const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads, int32_t kv_heads,
+                                 int32_t head_dim, int32_t causal, float sm_scale, void* out, float* lse,
+                                 uint32_t* status, void* stream);
+
+/* hpc_prompt_attention, causal, with the keys and values of request r in the pages of the cache: its
+ * seq_lens[r] cached tokens, the last cu_seqlens[r+1] - cu_seqlens[r] of which are the queries (a chunk of a
+ * prompt, or a prompt behind a cached prefix). BF16 caches, page_size 16, 32, 64 or 128; block_table and
+ * seq_lens as hpc_decode_attention. seq_lens[r] below the number of queries or beyond the block table sets
+ * HPC_DEV_BAD_SEQLEN and leaves the request out; a page id out of range sets HPC_DEV_BAD_PAGE, and the
+ * request's output is unspecified. */
+HPC_API int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                       const void* k_pages, const void* v_pages, hpc_dtype kv_dtype,
+                                       hpc_kv_layout kv_layout, int32_t num_pages, int32_t page_size,
+                                       const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
+                                       int64_t tokens, const int32_t* cu_seqlens, int32_t batch, int32_t num_heads,
+                                       int32_t kv_heads, int32_t head_dim, float sm_scale, void* out, float* lse,
+                                       uint32_t* status, void* stream);
+
 /* ---- verification of drafted tokens -----------------------------------------------------
  * After hpc_decode_step_multi has run the target over the drafted tokens: which of them stand, and the
  * token that follows. With p_t the target's and q_t the draft's probabilities at step t of request r,

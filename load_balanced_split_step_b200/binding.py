@@ -42,7 +42,7 @@ EXPORTS = ("hpc_step_record_bytes", "hpc_build_flags", "hpc_plan_workspace_bytes
            "hpc_decode_step_multi", "hpc_decode_step_multi_workspace_bytes", "hpc_decode_step_lse",
            "hpc_merge_lse", "hpc_wait_selftest", "hpc_merge_lse_gather", "hpc_gather_rows", "hpc_gather_pages",
            "hpc_prompt_prologue", "hpc_verify_drafts", "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact",
-           "hpc_pages_copy")
+           "hpc_pages_copy", "hpc_prompt_attention", "hpc_prompt_attention_paged")
 
 
 class HpcError(RuntimeError):
@@ -75,7 +75,7 @@ def _load(path=LIB):
         raise HpcError(f"{path} is missing; build it with `python -m load_balanced_split_step_b200.build` "
                        "(there is no CPU fallback)")
     lib = ctypes.CDLL(path)
-    i32, vp, sz = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
+    i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
     fp = ctypes.c_float
     P = ctypes.POINTER(CPlan)
     O = ctypes.POINTER(COptions)
@@ -123,6 +123,10 @@ def _load(path=LIB):
         "hpc_pages_fork": (ctypes.c_int, [vp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp, vp]),
         "hpc_pages_compact": (ctypes.c_int, [vp, vp, i32, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp]),
         "hpc_pages_copy": (ctypes.c_int, [ctypes.POINTER(vp), i32, ctypes.c_int64, i32, vp, i32, vp, vp, vp]),
+        "hpc_prompt_attention": (ctypes.c_int, [vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, vp, i32, i32, i32,
+                                                i32, i32, fp, vp, vp, vp, vp]),
+        "hpc_prompt_attention_paged": (ctypes.c_int, [vp, i64, i64, vp, vp, ctypes.c_int, ctypes.c_int, i32, i32, vp, i32,
+                                                      vp, i64, vp, i32, i32, i32, i32, fp, vp, vp, vp, vp]),
         "hpc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hpc_last_error": (ctypes.c_char_p, []),
         "hpc_abi_version": (ctypes.c_int, []),
@@ -768,6 +772,73 @@ def prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block
     return q_out, k_out, status
 
 
+def _strided(t, name, dev):
+    """A bf16 [tokens, heads, head_dim] tensor with contiguous heads; returns (token stride, head stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (dev is not None and t.device != dev):
+        raise HpcError(f"{name} must be a CUDA tensor" + ("" if dev is None else f" on {dev}"))
+    if t.dtype != torch.bfloat16:
+        raise HpcError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise HpcError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
+    n, H, D = t.shape
+    return (t.stride(0) if n > 1 else H * D), (t.stride(1) if H > 1 else D)
+
+
+def _lse(lse, return_lse, n, heads, dev):
+    if lse is None and not return_lse:
+        return None
+    return _buffer(lse, "lse", (n, heads), torch.float32, dev)
+
+
+def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_scale=None, out=None, lse=None,
+                     return_lse=False, status=None):
+    """Attention of packed prompts (``hpc_prompt_attention``): q [tokens, Hq, D], k / v [kv_tokens, Hkv, D] in
+    bf16, possibly views into one qkv tensor; sequence r is rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 (of k and
+    v: cu_seqlens_k, default the same), its queries the last of its keys. Returns (out bf16 [tokens, Hq, D],
+    lse fp32 [tokens, Hq] or None, status); rows of no sequence are left as they were."""
+    qs = _strided(q, "q", None)
+    dev = q.device
+    ks, vs = _strided(k, "k", dev), _strided(v, "v", dev)
+    n, Hq, D = q.shape
+    if tuple(v.shape) != tuple(k.shape) or k.shape[2] != D:
+        raise HpcError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must agree, with the query's head_dim {D}")
+    batch = _packed(cu_seqlens, dev)
+    if cu_seqlens_k is not None:
+        _packed(cu_seqlens_k, dev, batch)
+    out = _buffer(out, "out", (n, Hq, D), torch.bfloat16, dev)
+    lse = _lse(lse, return_lse, n, Hq, dev)
+    status = _status(status, dev)
+    scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_prompt_attention(_ptr(q), *qs, _ptr(k), *ks, _ptr(v), *vs, n, k.shape[0], _ptr(cu_seqlens),
+                                         _ptr(cu_seqlens_k), batch, Hq, k.shape[1], D, 1 if causal else 0, scale,
+                                         _ptr(out), _ptr(lse), _ptr(status), _stream(dev)), "hpc_prompt_attention")
+    return out, lse, status
+
+
+def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, *, kv_layout="HND", sm_scale=None,
+                           out=None, lse=None, return_lse=False, status=None):
+    """Causal attention of packed prompts, or chunks of them, over the bf16 pages of the cache
+    (``hpc_prompt_attention_paged``): the queries of request r are the last of its seq_lens[r] cached tokens.
+    Returns (out bf16 [tokens, Hq, D], lse fp32 [tokens, Hq] or None, status)."""
+    qs = _strided(q, "q", None)
+    dev = q.device
+    n, Hq, D = q.shape
+    code, num_pages, Hkv, P, lay = _cache(k_pages, v_pages, "bf16", kv_layout, None, None, D, dev)
+    batch = _packed(cu_seqlens, dev)
+    _tables(block_table, seq_lens, batch, dev)
+    out = _buffer(out, "out", (n, Hq, D), torch.bfloat16, dev)
+    lse = _lse(lse, return_lse, n, Hq, dev)
+    status = _status(status, dev)
+    scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    with torch.cuda.device(dev):
+        _check(_lib.hpc_prompt_attention_paged(
+            _ptr(q), *qs, _ptr(k_pages), _ptr(v_pages), code, lay, num_pages, P, _ptr(block_table),
+            block_table.shape[1], _ptr(seq_lens), n, _ptr(cu_seqlens), batch, Hq, Hkv, D, scale, _ptr(out), _ptr(lse),
+            _ptr(status), _stream(dev)), "hpc_prompt_attention_paged")
+    return out, lse, status
+
+
 def _rows(t, name, shape, dtype, dev):
     """A [batch, steps, vocab] tensor whose rows are equally far apart; returns that distance."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != dev:
@@ -946,7 +1017,7 @@ def copy_pages(caches, moves, n_moves, *, status=None):
     ptrs = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
     with torch.cuda.device(dev):
         _check(_lib.hpc_pages_copy(ptrs, len(caches), page_bytes, num_pages, _ptr(moves), moves.shape[0],
-                                   _ptr(n_moves), _ptr(status), _stream(dev)), "hpc_pages_copy")
+                                   _ptr(n_moves), _ptr(status), _stream(dev)), "hpc_pages_copy", "hpc_prompt_attention", "hpc_prompt_attention_paged")
     return status
 
 

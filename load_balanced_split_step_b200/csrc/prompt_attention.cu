@@ -1,0 +1,772 @@
+// Attention of whole prompts on the 5th-generation tensor cores: packed sequences, grouped heads,
+// causal, K and V packed or in the pages of the cache.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = 2^(c (s_ij - m_i)),   s_ij = q_i . k_j,   c = sm_scale log2 e
+// over the keys j that query i sees, in one pass over the keys with a running reference m_i.
+//
+// A unit of work is 256 query rows of one kv head: the group's G heads of 256 / G consecutive tokens of one
+// sequence, as two tiles A and B of 128 rows (row = G * token + head), so that a K or V block is
+// loaded once for all heads that share it. Per block of 128 keys each tile X takes two products,
+//   S_X[128 x 128] = Q_X . K^T      (tensor memory)
+//   O_X[128 x D]  += P_X . V        (P_X read from tensor memory, written over S_X)
+// with S_A, S_B, O_A, O_B filling the 512 columns of tensor memory. The tiles alternate: while the
+// tensor cores work on one, four warps run the softmax of the other, a thread per row, so that maxima and
+// sums cross no threads. The products are issued by one thread in the order P_A V, S_A', P_B V, S_B'. A new S
+// is issued only once the product that reads the P it overwrites has completed: different accumulators
+// are not ordered by the tensor pipe.
+//
+// m_i moves only when a block's maximum exceeds it by more than 8 (log2 units): p stays below 2^8, sums
+// and O are fp32, and the rescaling of O in tensor memory becomes rare. P is rounded to bf16 for its
+// product (relative error 2^-9 per weight, which the output's own bf16 rounding matches); the sum l_i is
+// taken over the unrounded values.
+//
+// Persistent CTAs (one per SM) take units longest first: units are put in 64 buckets by the number of
+// keys they reach and dealt in a snake over the CTAs, from a table that every CTA builds from cu_seqlens
+// at the start. The producer warp looks the units up, ahead of the others, and loads Q and
+// a ring of K and V blocks by TMA (swizzled planes of 64 elements).
+//
+// Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 one lane issues the
+// products, warp 9 looks up units and loads. A softmax thread holds the 128 scores of its row, so the
+// softmax warpgroups take registers from the third (216 + 216 + 72 = 3 x the 168 of the launch). Every
+// wait is bounded (2 s) and ends in HPC_DEV_TIMEOUT.
+#include <cmath>
+
+#include "umma_bf16.cuh"
+
+namespace hpc {
+namespace {
+
+constexpr int kPaThreads = 384;
+constexpr int kPaSoftRegs = 216, kPaOtherRegs = 72;
+constexpr int kPaMmaWarp = 8, kPaLoadWarp = 9;
+constexpr int kPaRows = 128;            // query rows per tile
+constexpr int kPaKeys = 128;            // keys per block
+constexpr int kPaPlane = 128 * 128;     // 128 rows of 64 bf16: one swizzled plane
+constexpr int kPaBuckets = 64;
+constexpr int kPaTileRing = 2;          // units looked up ahead
+constexpr uint32_t kPaCols = 512;       // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr float kPaMove = 8.f;
+constexpr int kPaStages64 = 8, kPaStages128 = 5;
+
+template <int D>
+struct PaLayout {
+  static constexpr int kPlanes = D / 64;
+  static constexpr int kStages = D == 128 ? kPaStages128 : kPaStages64;
+  static constexpr int kTile = kPlanes * kPaPlane;  // a Q tile, a K block or a V block
+  static constexpr int kOffRing = 2 * kTile;
+  static constexpr int kBytes = kOffRing + kStages * kTile + 1024;  // + alignment slack
+};
+
+// One unit of work, as the producer publishes it.
+struct PaUnit {
+  int32_t valid;
+  int32_t q0, q_end;  // row of q of the first token; end of the sequence
+  int32_t kv0;        // packed: row of key 0; paged: the request
+  int32_t keys;       // keys of the sequence
+  int32_t vis;        // keys that the unit's first token sees, one more for each token after it
+  int32_t blocks[2];  // key blocks of tile A and B
+  int32_t kvh;
+  int32_t pad[3];
+};
+
+struct PaArgs {
+  const int32_t* cu_q;
+  const int32_t* cu_k;      // packed
+  const int32_t* table;     // paged
+  const int32_t* seq_lens;  // paged
+  __nv_bfloat16* out;
+  float* lse;
+  uint32_t* status;
+  int64_t tokens, kv_tokens, max_pages;
+  float scale_log2, scale;
+  int32_t batch, Hq, Hkv, group, causal, P, num_pages, nhd;
+};
+
+struct PaBars {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full, q_free;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t unit_full[kPaTileRing], unit_free[kPaTileRing];
+  uint64_t drained;
+};
+
+struct PaShared {
+  PaBars bars;
+  PaUnit unit[kPaTileRing];
+  int32_t base[kPaBuckets];   // units' token tiles in the buckets above
+  int32_t count[kPaBuckets];
+  int32_t hist[kPaBuckets + 1], rem[kPaBuckets + 1];
+  int32_t span;               // extent of the cost axis
+  int32_t tiles;              // all token tiles
+  int32_t bad;
+  uint32_t tmem;
+};
+
+// A sequence's tokens and keys; false when the lengths do not hold together.
+__device__ __forceinline__ bool pa_sequence(const PaArgs& a, bool paged, int32_t s, int32_t& q0, int32_t& q1, int32_t& k0,
+                                            int32_t& keys) {
+  q0 = a.cu_q[s];
+  q1 = a.cu_q[s + 1];
+  bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.tokens;
+  if (paged) {
+    k0 = s;
+    keys = a.seq_lens[s];
+    ok = ok && keys >= q1 - q0 && static_cast<int64_t>(keys) <= a.max_pages * a.P;
+  } else {
+    k0 = a.cu_k[s];
+    const int32_t k1 = a.cu_k[s + 1];
+    keys = k1 - k0;
+    ok = ok && k0 >= 0 && k1 >= k0 && k1 <= a.kv_tokens;
+  }
+  if (!ok) q0 = q1 = keys = 0;
+  return ok;
+}
+
+// The sequence's token tiles on the cost axis [lo, hi): a tile costs the tiles' worth of keys it reaches.
+__device__ __forceinline__ void pa_span(const PaArgs& a, int32_t q0, int32_t q1, int32_t keys, int32_t tile_tokens,
+                                        int32_t& lo, int32_t& hi) {
+  const int32_t n = q1 - q0, before = a.causal ? (keys > n ? keys - n : 0) : keys;
+  lo = before / tile_tokens;
+  hi = lo + (n + tile_tokens - 1) / tile_tokens;
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const PaArgs a) {
+  using L = PaLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PaShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + L::kOffRing;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t tokens_per_tile = kPaRows / a.group, tokens_per_unit = 2 * tokens_per_tile;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(bar(sh.bars.kv_full[s]), 1);
+      mbar_init(bar(sh.bars.kv_empty[s]), 1);
+    }
+    mbar_init(bar(sh.bars.q_full), 1);
+    mbar_init(bar(sh.bars.q_free), 1);
+    mbar_init(bar(sh.bars.drained), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(sh.bars.s_full[x]), 1);
+      mbar_init(bar(sh.bars.p_full[x]), 4);
+      mbar_init(bar(sh.bars.pv_done[x]), 1);
+    }
+    for (int t = 0; t < kPaTileRing; ++t) {
+      mbar_init(bar(sh.bars.unit_full[t]), 1);
+      mbar_init(bar(sh.bars.unit_free[t]), 9);  // 8 softmax warps and the issuing thread
+    }
+    fence_barrier_init();
+    sh.span = 0;
+    sh.bad = 0;
+  }
+  for (int i = threadIdx.x; i <= kPaBuckets; i += kPaThreads) sh.hist[i] = sh.rem[i] = 0;
+  if (warp == kPaMmaWarp) tmem_alloc(smem_u32(&sh.tmem), kPaCols);
+  if (warp == kPaLoadWarp && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the table of units: 64 buckets of the cost axis
+  {
+    int32_t span = 0, bad = 0;
+    for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
+      int32_t q0, q1, k0, keys, lo, hi;
+      bad |= !pa_sequence(a, kPaged, s, q0, q1, k0, keys);
+      pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
+      if (hi > span) span = hi;
+    }
+    atomicMax(&sh.span, span);
+    if (bad) sh.bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.bad && blockIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
+  }
+  const int32_t width = (sh.span + kPaBuckets - 1) / kPaBuckets > 0 ? (sh.span + kPaBuckets - 1) / kPaBuckets : 1;
+  for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
+    int32_t q0, q1, k0, keys, lo, hi;
+    pa_sequence(a, kPaged, s, q0, q1, k0, keys);
+    pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
+    if (hi > lo) {
+      atomicAdd(&sh.hist[hi / width], 1);
+      atomicAdd(&sh.rem[hi / width], hi % width);
+      atomicAdd(&sh.hist[lo / width], -1);
+      atomicAdd(&sh.rem[lo / width], -(lo % width));
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // longest first: lane l holds the buckets 63 - 2 l and 62 - 2 l
+    const int b0 = kPaBuckets - 1 - 2 * lane, b1 = b0 - 1;
+    auto scan = [&](int32_t v) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      return v;
+    };
+    const int32_t h0 = sh.hist[b0], h1 = sh.hist[b1];
+    const int32_t above = sh.hist[kPaBuckets] + scan(h0 + h1) - h0 - h1;  // sequences that end past bucket b0
+    const int32_t c0 = above * width + sh.rem[b0], c1 = (above + h0) * width + sh.rem[b1];
+    const int32_t upto = scan(c0 + c1);
+    sh.count[b0] = c0;
+    sh.count[b1] = c1;
+    sh.base[b0] = upto - c0 - c1;
+    sh.base[b1] = upto - c1;
+    if (lane == 31) sh.tiles = upto;
+  }
+  __syncthreads();
+  const int64_t units = static_cast<int64_t>(sh.tiles) * a.Hkv;
+  bool ok = true;
+  uint32_t err = 0;
+  auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
+    if (ok && !mbar_wait(smem_u32(&b), parity)) {
+      ok = false;
+      err = HPC_DEV_TIMEOUT;
+    }
+    return ok;
+  };
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPaSoftRegs));
+    // ------------------------------------------------------------------ softmax, tile t of every unit
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
+    const int32_t tok = t * tokens_per_tile + row / a.group;
+    const int32_t head_in = row % a.group;
+    const float c = a.scale_log2;
+    uint32_t done = 0;  // blocks of this tile so far
+    uint32_t fill = 0;  // ring stages of the units before
+    for (int32_t n_unit = 0;; ++n_unit) {
+      const int slot = n_unit % kPaTileRing;
+      wait(sh.bars.unit_full[slot], (n_unit / kPaTileRing) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const PaUnit x = sh.unit[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.bars.unit_free[slot]));
+      if (!x.valid) break;
+      const int nb = t == 0 ? x.blocks[0] : x.blocks[1];
+      const int nb_unit = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
+      // keys this row sees; fewest of the tile's rows
+      int32_t vis = a.causal ? x.vis + tok : x.keys;
+      if (vis > x.keys) vis = x.keys;
+      int32_t vis_min = a.causal ? x.vis + t * tokens_per_tile : x.keys;
+      if (vis_min > x.keys) vis_min = x.keys;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nb && ok; ++j) {
+        wait(sh.bars.s_full[t], done & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float v[128];
+        umma::ld128(s_at, v);
+        if ((j + 1) * kPaKeys > vis_min) {
+          const int32_t lim = vis - j * kPaKeys;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i] = i < lim ? v[i] : -INFINITY;
+        }
+        float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+#pragma unroll
+        for (int i = 4; i < 128; i += 8) {
+          x0 = fmaxf(fmaxf(x0, v[i]), v[i + 1]);
+          x1 = fmaxf(fmaxf(x1, v[i + 2]), v[i + 3]);
+          if (i + 4 < 128) {
+            x2 = fmaxf(fmaxf(x2, v[i + 4]), v[i + 5]);
+            x3 = fmaxf(fmaxf(x3, v[i + 6]), v[i + 7]);
+          }
+        }
+        const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+        // the reference: set by the first block with a key, then moved only past the margin
+        bool move = false;
+        float shrink = 1.f;
+        if (mx > m) {
+          if (m == -INFINITY) {
+            m = mx;
+          } else if ((mx - m) * c > kPaMove) {
+            shrink = ex2((m - mx) * c);
+            m = mx;
+            l *= shrink;
+            move = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          // O in tensor memory; the product of the block before has completed (this block's S waited for it)
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            umma::ld32(o_at + c0, o);
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * shrink);
+            umma::st32(o_at + c0, w);
+          }
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+        float2 sum[4] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float2 e = fma2(make_float2(v[64 * h + 2 * i], v[64 * h + 2 * i + 1]), c2, mc2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[i & 3] = add2(sum[i & 3], e);
+            w[i] = pack_bf16x2(e.x, e.y);
+          }
+          umma::st32(s_at + 32 * h, w);
+        }
+        const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += s2.x + s2.y;
+        if ((j + 1) * kPaKeys > x.keys && (t == 0 || j >= x.blocks[0])) {
+          // Rows of V past the last key hold another sequence's values or what the memory held: zero, so that
+          // 0 * v stays 0. The fill is the only one that its parity can mean: the stage's fill before was read
+          // by products that this block's S follows.
+          const uint32_t f = fill + 2 * j + 1;
+          wait(sh.bars.kv_full[f % L::kStages], (f / L::kStages) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          uint8_t* vt = ring + (f % L::kStages) * L::kTile;
+          const int32_t first = x.keys - j * kPaKeys;
+          for (int i = threadIdx.x & 127; i < (kPaKeys - first) * 8; i += 128)
+            for (int pl = 0; pl < L::kPlanes; ++pl)
+              *reinterpret_cast<uint4*>(vt + pl * kPaPlane + first * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_shared();
+        }
+        umma::st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.bars.p_full[t]));
+        ++done;
+      }
+      fill += 2 * nb_unit;
+      // ---- epilogue
+      if (nb > 0) {
+        wait(sh.bars.pv_done[t], (done - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool live = x.q0 + tok < x.q_end;
+      const int64_t at = static_cast<int64_t>(x.q0 + tok) * a.Hq + x.kvh * a.group + head_in;
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a NaN stays one; a row without keys is zero
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        float o[32];
+        if (nb > 0) {
+          umma::ld32(o_at + c0, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        }
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + c0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        }
+      }
+      if (a.lse && live) a.lse[at] = l > 0.f || l != l ? m * a.scale + logf(l) : -INFINITY;
+      tc_fence_before();
+    }
+    if (err && lane == 0) atomicOr(a.status, err);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPaOtherRegs));
+    if (warp == kPaLoadWarp) {
+      // ------------------------------------------------------------------ units and loads
+      uint32_t fill = 0;  // ring fills so far
+      int32_t n_unit = 0, n_q = 0;
+      for (int64_t k = 0;; ++k) {
+        // the k-th unit of this CTA, in a snake over the CTAs
+        const int64_t u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        PaUnit x = {};
+        x.valid = u < units;
+        if (x.valid) {
+          const int32_t tile = static_cast<int32_t>(u / a.Hkv);
+          x.kvh = static_cast<int32_t>(u - static_cast<int64_t>(tile) * a.Hkv);
+          // bucket: the one with base <= tile < base + count
+          uint32_t m0 = __ballot_sync(0xffffffffu, tile >= sh.base[lane] && tile < sh.base[lane] + sh.count[lane]);
+          uint32_t m1 = __ballot_sync(0xffffffffu, tile >= sh.base[lane + 32] && tile < sh.base[lane + 32] + sh.count[lane + 32]);
+          const int b = m0 ? __ffs(m0) - 1 : 32 + __ffs(m1) - 1;
+          int32_t rank = tile - sh.base[b];
+          // sequence: prefix of the tiles that each has in the bucket
+          for (int32_t s0 = 0; s0 < a.batch; s0 += 32) {
+            const int32_t s = s0 + lane;
+            int32_t q0 = 0, q1 = 0, k0 = 0, keys = 0, lo = 0, hi = 0, from = 0, n = 0;
+            if (s < a.batch) {
+              pa_sequence(a, kPaged, s, q0, q1, k0, keys);
+              pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
+              from = lo > b * width ? lo : b * width;
+              const int32_t to = hi < (b + 1) * width ? hi : (b + 1) * width;
+              n = to > from ? to - from : 0;
+            }
+            int32_t inc = n;
+  #pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+              if (lane >= o) inc += y;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, rank < inc);
+            if (hit) {
+              const int w = __ffs(hit) - 1;
+              const int32_t i = __shfl_sync(0xffffffffu, from - lo + rank - (inc - n), w);
+              q0 = __shfl_sync(0xffffffffu, q0, w);
+              q1 = __shfl_sync(0xffffffffu, q1, w);
+              keys = __shfl_sync(0xffffffffu, keys, w);
+              x.kv0 = __shfl_sync(0xffffffffu, k0, w);
+              x.q0 = q0 + i * tokens_per_unit;
+              x.q_end = q1;
+              x.keys = keys;
+              x.vis = a.causal ? keys - (q1 - q0) + i * tokens_per_unit + 1 : keys;
+              for (int t = 0; t < 2; ++t) {
+                // the last token of the tile that exists sees the most
+                const int32_t first = x.q0 + t * tokens_per_tile;
+                const int32_t last = first + tokens_per_tile < q1 ? first + tokens_per_tile : q1;
+                int32_t seen = a.causal ? x.vis + (last - 1 - x.q0) : keys;
+                if (seen > keys) seen = keys;
+                x.blocks[t] = first < q1 && seen > 0 ? (seen + kPaKeys - 1) / kPaKeys : 0;
+              }
+              break;
+            }
+            rank -= __shfl_sync(0xffffffffu, inc, 31);
+          }
+        }
+        const int slot = n_unit % kPaTileRing;
+        if (n_unit >= kPaTileRing) wait(sh.bars.unit_free[slot], ((n_unit / kPaTileRing) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) x.valid = 0;
+        if (lane == 0) {
+          sh.unit[slot] = x;
+          mbar_arrive(bar(sh.bars.unit_full[slot]));
+        }
+        ++n_unit;
+        if (!x.valid) break;
+        const int nb = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
+        if (nb == 0) continue;  // no keys: the epilogue writes zeros
+        // Q, once the products of the unit before have read theirs
+        if (n_q > 0) wait(sh.bars.q_free, (n_q - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++n_q;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(sh.bars.q_full), 2 * L::kTile);
+          for (int t = 0; t < 2; ++t)
+            for (int pl = 0; pl < L::kPlanes; ++pl)
+              tma_load_4d(smem_u32(smem) + t * L::kTile + pl * kPaPlane, &tm_q, bar(sh.bars.q_full), 64 * pl,
+                          x.kvh * a.group, x.q0 + t * tokens_per_tile, 0);
+        }
+        // K_0, V_0, K_1, V_1, ...
+        if (!kPaged) {
+          if (lane == 0) {
+            for (int f = 0; f < 2 * nb && ok; ++f, ++fill) {
+              const int st = fill % L::kStages;
+              if (fill >= L::kStages && !wait(sh.bars.kv_empty[st], (fill / L::kStages - 1) & 1)) break;
+              mbar_arrive_expect_tx(bar(sh.bars.kv_full[st]), L::kTile);
+              for (int pl = 0; pl < L::kPlanes; ++pl)
+                tma_load_4d(smem_u32(ring) + st * L::kTile + pl * kPaPlane, (f & 1) ? &tm_v : &tm_k,
+                            bar(sh.bars.kv_full[st]), 64 * pl, x.kvh, x.kv0 + (f >> 1) * kPaKeys, 0);
+            }
+          }
+        } else {
+          // 32 page ids at a time; pages of one block never straddle two batches of ids
+          const int32_t* row = a.table + static_cast<int64_t>(x.kv0) * a.max_pages;
+          const int per_block = kPaKeys / a.P;
+          const int32_t live = (x.keys + a.P - 1) / a.P;  // pages that hold keys
+          for (int32_t p0 = 0; p0 < nb * per_block && ok; p0 += 32) {
+            int32_t id = 0;
+            if (p0 + lane < live && p0 + lane < nb * per_block) {
+              id = row[p0 + lane];
+              if (id < 0 || id >= a.num_pages) {
+                id = 0;
+                err |= HPC_DEV_BAD_PAGE;  // a stand-in; the request's output is unspecified
+              }
+            }
+            const int blocks = (nb * per_block - p0 < 32 ? nb * per_block - p0 : 32) / per_block;
+            for (int f = 0; f < 2 * blocks && ok; ++f, ++fill) {
+              const int st = fill % L::kStages;
+              if (fill >= L::kStages) wait(sh.bars.kv_empty[st], (fill / L::kStages - 1) & 1);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const int first = (f >> 1) * per_block;
+              const int n = live - p0 - first < per_block ? live - p0 - first : per_block;
+              if (lane == 0) mbar_arrive_expect_tx(bar(sh.bars.kv_full[st]), n * L::kPlanes * a.P * 128);
+              __syncwarp();
+              if (lane >= first && lane < first + n) {
+                const uint32_t dst = smem_u32(ring) + st * L::kTile + (lane - first) * a.P * 128;
+                for (int pl = 0; pl < L::kPlanes; ++pl)
+                  tma_load_4d(dst + pl * kPaPlane, (f & 1) ? &tm_v : &tm_k, bar(sh.bars.kv_full[st]), 64 * pl,
+                              a.nhd ? x.kvh : 0, a.nhd ? 0 : x.kvh, id);
+              }
+            }
+          }
+        }
+        fill = __shfl_sync(0xffffffffu, fill, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      // every load has to land before the CTA may exit
+      if (lane == 0) {
+        if (n_q > 0 && !mbar_wait(bar(sh.bars.q_full), (n_q - 1) & 1)) err |= HPC_DEV_TIMEOUT;
+        for (uint32_t f = fill > L::kStages ? fill - L::kStages : 0; f < fill; ++f)
+          if (!mbar_wait(bar(sh.bars.kv_full[f % L::kStages]), (f / L::kStages) & 1)) err |= HPC_DEV_TIMEOUT;
+      }
+      if (err) atomicOr(a.status, err);
+      __syncwarp();
+    } else if (warp == kPaMmaWarp) {
+      // ------------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t kIdS = umma::idesc(128, 128, false), kIdO = umma::idesc(128, D, true);
+        uint32_t fill = 0;          // ring stages consumed (released) so far
+        uint32_t done[2] = {0, 0};  // blocks of tile A, B issued so far: phases of s_full, p_full, pv_done
+        int32_t n_q = 0;
+        auto full = [&](uint32_t f) { return wait(sh.bars.kv_full[f % L::kStages], (f / L::kStages) & 1); };
+        auto scores = [&](int t, uint32_t f) {  // S_t = Q_t . K^T of ring fill f
+          const uint32_t q = smem_u32(smem) + t * L::kTile, k = smem_u32(ring) + (f % L::kStages) * L::kTile;
+          tc_fence_after();
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int off = (kk >> 2) * kPaPlane + 32 * (kk & 3);
+            umma::mma_ss(tmem + 128 * t, umma_desc(q + off, 16, 1024, 2), umma_desc(k + off, 16, 1024, 2), kIdS, kk > 0);
+          }
+          umma_commit(bar(sh.bars.s_full[t]));
+        };
+        for (int32_t n_unit = 0;; ++n_unit) {
+          const int slot = n_unit % kPaTileRing;
+          if (!wait(sh.bars.unit_full[slot], (n_unit / kPaTileRing) & 1)) break;
+          const PaUnit x = sh.unit[slot];
+          mbar_arrive(bar(sh.bars.unit_free[slot]));
+          if (!x.valid) break;
+          const int nb = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
+          if (nb == 0) continue;
+          if (!wait(sh.bars.q_full, n_q & 1)) break;
+          ++n_q;
+          for (int j = 0; j <= nb && ok; ++j) {
+            // fill + 2 j is K_j, fill + 2 j - 1 is V_{j-1}
+            if (j > 0 && !full(fill + 2 * j - 1)) break;
+            if (j < nb && !full(fill + 2 * j)) break;
+            for (int t = 0; t < 2; ++t) {
+              if (j > 0 && j - 1 < x.blocks[t]) {
+                if (!wait(sh.bars.p_full[t], (done[t] - 1) & 1)) break;
+                tc_fence_after();
+                const uint32_t v = smem_u32(ring) + ((fill + 2 * j - 1) % L::kStages) * L::kTile;
+  #pragma unroll
+                for (int kk = 0; kk < kPaKeys / 16; ++kk)
+                  umma::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, umma_desc(v + 2048 * kk, kPaPlane, 1024, 2), kIdO,
+                               (j > 1 || kk > 0) ? 1u : 0u);
+                umma_commit(bar(sh.bars.pv_done[t]));
+              }
+              if (t == 1 && j > 0) umma_commit(bar(sh.bars.kv_empty[(fill + 2 * j - 1) % L::kStages]));
+              if (j < x.blocks[t]) {
+                // the product that reads the P which this S overwrites
+                if (done[t] > 0 && !wait(sh.bars.pv_done[t], (done[t] - 1) & 1)) break;
+                scores(t, fill + 2 * j);
+                ++done[t];
+              }
+              if (t == 1 && j < nb) umma_commit(bar(sh.bars.kv_empty[(fill + 2 * j) % L::kStages]));
+            }
+            if (j == nb - 1) umma_commit(bar(sh.bars.q_free));  // the last read of Q
+          }
+          fill += 2 * nb;
+        }
+        // the products in flight read shared and tensor memory
+        umma_commit(bar(sh.bars.drained));
+        if (!mbar_wait(bar(sh.bars.drained), 0)) err |= HPC_DEV_TIMEOUT;
+        if (err) atomicOr(a.status, err);
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPaMmaWarp) {
+    tc_fence_after();
+    tmem_free(tmem, kPaCols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 pa_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  return fn;
+}
+
+// A map of 128-byte swizzled boxes [box3][box2][box1][64 elements].
+int pa_map(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+           const uint32_t (&box)[4]) {
+  auto fn = pa_encode();
+  if (!fn) return fail(HPC_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const uint32_t ones[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+                        reinterpret_cast<const cuuint64_t*>(dims), reinterpret_cast<const cuuint64_t*>(strides),
+                        reinterpret_cast<const cuuint32_t*>(box), reinterpret_cast<const cuuint32_t*>(ones),
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(HPC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return HPC_OK;
+}
+
+// [tokens][heads][D] with the given strides (elements), in boxes of `box_heads` x `box_tokens`.
+int pa_packed_map(CUtensorMap* map, const void* base, int64_t tokens, int32_t heads, int32_t D, int64_t token_stride,
+                  int64_t head_stride, uint32_t box_heads, uint32_t box_tokens) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens), 1};
+  const uint64_t strides[3] = {static_cast<uint64_t>(head_stride) * 2, static_cast<uint64_t>(token_stride) * 2,
+                               static_cast<uint64_t>(token_stride) * 2 * static_cast<uint64_t>(tokens)};
+  const uint32_t box[4] = {64, box_heads, box_tokens, 1};
+  return pa_map(map, base, dims, strides, box);
+}
+
+template <int D, bool kPaged>
+int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PaArgs& a, cudaStream_t stream) {
+  using L = PaLayout<D>;
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  auto kern = prompt_attention_kernel<D, kPaged>;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
+      return check_launch("cudaFuncSetAttribute(prompt_attention_kernel)");
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
+  const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+  // units: at most one part-filled per sequence and kv head
+  const int64_t per_unit = 2 * kPaRows / a.group;
+  const int64_t most = (a.tokens / per_unit + (a.batch < a.tokens ? a.batch : a.tokens)) * a.Hkv;
+  const int grid = static_cast<int>(most < sms ? most : sms);
+  const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kPaThreads), static_cast<size_t>(L::kBytes), stream, q, k, v, a);
+  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_attention_kernel: %s", cudaGetErrorString(e));
+  return check_launch("prompt_attention_kernel");
+}
+
+// What both entry points check of the queries and the shape; fills the common arguments and q's map.
+int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t tokens, const int32_t* cu_seqlens,
+              int32_t batch, int32_t num_heads, int32_t kv_heads, int32_t head_dim, float sm_scale, void* out,
+              float* lse, uint32_t* status, PaArgs& a, CUtensorMap* map) {
+  if (tokens < 0 || tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "tokens out of range");
+  if (!cu_seqlens || !status || (tokens > 0 && (!q || !out))) return fail(HPC_ERR_ARG, "null pointer argument");
+  if (batch < 1 || num_heads < 1 || kv_heads < 1) return fail(HPC_ERR_ARG, "sizes must be >= 1");
+  if (num_heads % kv_heads) return fail(HPC_ERR_SHAPE, "num_heads %% kv_heads != 0");
+  const int32_t g = num_heads / kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8) return fail(HPC_ERR_SHAPE, "num_heads / kv_heads must be 1, 2, 4 or 8");
+  if (head_dim != 64 && head_dim != 128) return fail(HPC_ERR_SHAPE, "head_dim must be 64 or 128");
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return fail(HPC_ERR_ARG, "sm_scale must be positive and finite");
+  a.cu_q = cu_seqlens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.status = status;
+  a.tokens = tokens;
+  a.scale = sm_scale;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.batch = batch;
+  a.Hq = num_heads;
+  a.Hkv = kv_heads;
+  a.group = g;
+  if (tokens == 0) return HPC_OK;
+  if (!aligned16(q) || !aligned16(out)) return fail(HPC_ERR_ALIGN, "q and out must be 16-byte aligned");
+  if (q_token_stride % 8 || q_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0)
+    return fail(HPC_ERR_ALIGN, "strides must be multiples of 8 elements");
+  return pa_packed_map(map, q, tokens, num_heads, head_dim, q_token_stride, q_head_stride, g, kPaRows / g);
+}
+
+}  // namespace
+}  // namespace hpc
+
+using namespace hpc;
+
+extern "C" int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                                    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                    int64_t v_head_stride, int64_t tokens, int64_t kv_tokens, const int32_t* cu_seqlens,
+                                    const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads, int32_t kv_heads,
+                                    int32_t head_dim, int32_t causal, float sm_scale, void* out, float* lse,
+                                    uint32_t* status, void* stream) {
+  PaArgs a = {};
+  CUtensorMap mq, mk, mv;
+  int rc = pa_common(q, q_token_stride, q_head_stride, tokens, cu_seqlens, batch, num_heads, kv_heads, head_dim, sm_scale,
+                     out, lse, status, a, &mq);
+  if (rc != HPC_OK) return rc;
+  if (kv_tokens < 0 || kv_tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "kv_tokens out of range");
+  if (!cu_seqlens_k && kv_tokens != tokens)
+    return fail(HPC_ERR_ARG, "without cu_seqlens_k the keys are the tokens (kv_tokens == tokens)");
+  if (kv_tokens > 0 && (!k || !v)) return fail(HPC_ERR_ARG, "null pointer argument");
+  if (tokens == 0) return HPC_OK;
+  if (!aligned16(k) || !aligned16(v)) return fail(HPC_ERR_ALIGN, "k and v must be 16-byte aligned");
+  if ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 || k_token_stride < 0 || k_head_stride < 0 ||
+      v_token_stride < 0 || v_head_stride < 0)
+    return fail(HPC_ERR_ALIGN, "strides must be multiples of 8 elements");
+  a.cu_k = cu_seqlens_k ? cu_seqlens_k : cu_seqlens;
+  a.kv_tokens = kv_tokens;
+  a.causal = causal != 0;
+  if (kv_tokens > 0) {
+    if ((rc = pa_packed_map(&mk, k, kv_tokens, kv_heads, head_dim, k_token_stride, k_head_stride, 1, kPaKeys)) != HPC_OK)
+      return rc;
+    if ((rc = pa_packed_map(&mv, v, kv_tokens, kv_heads, head_dim, v_token_stride, v_head_stride, 1, kPaKeys)) != HPC_OK)
+      return rc;
+  } else {
+    mk = mv = mq;  // never loaded from: no sequence has keys
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? pa_launch<128, false>(mq, mk, mv, a, st) : pa_launch<64, false>(mq, mk, mv, a, st);
+}
+
+extern "C" int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                          const void* k_pages, const void* v_pages, hpc_dtype kv_dtype,
+                                          hpc_kv_layout kv_layout, int32_t num_pages, int32_t page_size,
+                                          const int32_t* block_table, int32_t max_pages_per_req,
+                                          const int32_t* seq_lens, int64_t tokens, const int32_t* cu_seqlens,
+                                          int32_t batch, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+                                          float sm_scale, void* out, float* lse, uint32_t* status, void* stream) {
+  PaArgs a = {};
+  CUtensorMap mq, mk, mv;
+  int rc = pa_common(q, q_token_stride, q_head_stride, tokens, cu_seqlens, batch, num_heads, kv_heads, head_dim, sm_scale,
+                     out, lse, status, a, &mq);
+  if (rc != HPC_OK) return rc;
+  if (!k_pages || !v_pages || !block_table || !seq_lens) return fail(HPC_ERR_ARG, "null pointer argument");
+  if (kv_dtype != HPC_BF16) return fail(HPC_ERR_DTYPE, "the paged prompt attention reads BF16 caches");
+  if (kv_layout != HPC_HND && kv_layout != HPC_NHD) return fail(HPC_ERR_ARG, "kv_layout must be HND or NHD");
+  if (num_pages < 1 || max_pages_per_req < 1) return fail(HPC_ERR_ARG, "sizes must be >= 1");
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+    return fail(HPC_ERR_SHAPE, "page_size must be 16, 32, 64 or 128");
+  if (static_cast<int64_t>(max_pages_per_req) * page_size > INT32_MAX - 1024)
+    return fail(HPC_ERR_SHAPE, "max_pages_per_req x page_size out of range");
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return fail(HPC_ERR_ALIGN, "caches must be 16-byte aligned");
+  if (tokens == 0) return HPC_OK;
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.max_pages = max_pages_per_req;
+  a.P = page_size;
+  a.num_pages = num_pages;
+  a.nhd = kv_layout == HPC_NHD;
+  a.causal = 1;
+  const uint64_t D = head_dim, H = kv_heads, P = page_size;
+  const uint64_t dims[4] = {D, a.nhd ? H : P, a.nhd ? P : H, static_cast<uint64_t>(num_pages)};
+  const uint64_t strides[3] = {D * 2, D * 2 * dims[1], D * 2 * H * P};
+  const uint32_t box[4] = {64, a.nhd ? 1u : static_cast<uint32_t>(P), a.nhd ? static_cast<uint32_t>(P) : 1u, 1};
+  if ((rc = pa_map(&mk, k_pages, dims, strides, box)) != HPC_OK) return rc;
+  if ((rc = pa_map(&mv, v_pages, dims, strides, box)) != HPC_OK) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return head_dim == 128 ? pa_launch<128, true>(mq, mk, mv, a, st) : pa_launch<64, true>(mq, mk, mv, a, st);
+}
