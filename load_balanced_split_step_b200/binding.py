@@ -722,11 +722,38 @@ def _packed(cu_seqlens, dev, batch=None):
     return n
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_words = {}  # (device, stream) -> status words zeroed there and not handed out yet
+
+
 def _status(status, dev):
-    if status is None:
+    """The caller's status word, or a zeroed one. Words are zeroed 64 at a time on the stream that will use
+    them: a memset of its own for each call costs as much as a small kernel. A captured call zeroes its
+    own word, at every replay."""
+    if status is not None:
+        _need(status, "status", torch.int32, dev)
+        return status
+    if torch.cuda.is_current_stream_capturing():
         return new_status(dev)
-    _need(status, "status", torch.int32, dev)
-    return status
+    words = _words.setdefault((dev.index, torch._C._cuda_getCurrentRawStream(dev.index)), [])
+    try:
+        return words.pop()
+    except IndexError:
+        words.extend(torch.zeros(64, dtype=torch.int32, device=dev).split(1))
+        return words.pop()
+
+
+def _launch(name, dev, *args):
+    """Calls a library function that ends in a stream, on the current stream of the tensors' device."""
+    if torch.cuda.current_device() == dev.index:
+        rc = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(rc, name)
 
 
 def _buffer(t, name, shape, dtype, dev):
@@ -763,12 +790,10 @@ def prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block
     q_out = _buffer(q_out, "q_out", (n, num_heads, D), torch.bfloat16, dev)
     k_out = _buffer(k_out, "k_out", (n, kv_heads, D), torch.bfloat16, dev)
     status = _status(status, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_prompt_prologue(
-            _ptr(qkv), n, _ptr(cu_seqlens), batch, _ptr(q_norm_w), _ptr(k_norm_w), float(eps), float(rope_theta),
-            _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), code, lay, _ptr(k_scale), _ptr(v_scale), num_pages,
-            P, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), num_heads, kv_heads, D, _ptr(status),
-            _stream(dev)), "hpc_prompt_prologue")
+    _launch("hpc_prompt_prologue", dev, _addr(qkv), n, _addr(cu_seqlens), batch, _addr(q_norm_w), _addr(k_norm_w),
+            float(eps), float(rope_theta), _addr(q_out), _addr(k_out), _addr(k_pages), _addr(v_pages), code, lay,
+            _addr(k_scale), _addr(v_scale), num_pages, P, _addr(block_table), block_table.shape[1], _addr(seq_lens),
+            num_heads, kv_heads, D, _addr(status))
     return q_out, k_out, status
 
 
@@ -809,10 +834,9 @@ def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_
     lse = _lse(lse, return_lse, n, Hq, dev)
     status = _status(status, dev)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_prompt_attention(_ptr(q), *qs, _ptr(k), *ks, _ptr(v), *vs, n, k.shape[0], _ptr(cu_seqlens),
-                                         _ptr(cu_seqlens_k), batch, Hq, k.shape[1], D, 1 if causal else 0, scale,
-                                         _ptr(out), _ptr(lse), _ptr(status), _stream(dev)), "hpc_prompt_attention")
+    _launch("hpc_prompt_attention", dev, _addr(q), *qs, _addr(k), *ks, _addr(v), *vs, n, k.shape[0], _addr(cu_seqlens),
+            _addr(cu_seqlens_k), batch, Hq, k.shape[1], D, 1 if causal else 0, scale, _addr(out), _addr(lse),
+            _addr(status))
     return out, lse, status
 
 
@@ -831,11 +855,9 @@ def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlen
     lse = _lse(lse, return_lse, n, Hq, dev)
     status = _status(status, dev)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_prompt_attention_paged(
-            _ptr(q), *qs, _ptr(k_pages), _ptr(v_pages), code, lay, num_pages, P, _ptr(block_table),
-            block_table.shape[1], _ptr(seq_lens), n, _ptr(cu_seqlens), batch, Hq, Hkv, D, scale, _ptr(out), _ptr(lse),
-            _ptr(status), _stream(dev)), "hpc_prompt_attention_paged")
+    _launch("hpc_prompt_attention_paged", dev, _addr(q), *qs, _addr(k_pages), _addr(v_pages), code, lay, num_pages, P,
+            _addr(block_table), block_table.shape[1], _addr(seq_lens), n, _addr(cu_seqlens), batch, Hq, Hkv, D, scale,
+            _addr(out), _addr(lse), _addr(status))
     return out, lse, status
 
 
@@ -889,12 +911,9 @@ def verify_drafts(draft_tokens, target_probs, draft_probs, uniforms, *, draft_le
     elif new_lens is not None:
         raise HpcError("new_lens needs seq_lens")
     status = _status(status, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_verify_drafts(
-            _ptr(draft_tokens), _ptr(target_probs), p_row, _ptr(draft_probs), q_row,
-            HPC_FP32 if target_probs.dtype == torch.float32 else HPC_BF16, _ptr(uniforms), _ptr(draft_lens),
-            _ptr(seq_lens), Bn, T, V, _ptr(out_tokens), _ptr(accepted), _ptr(new_lens), _ptr(status), _stream(dev)),
-            "hpc_verify_drafts")
+    _launch("hpc_verify_drafts", dev, _addr(draft_tokens), _addr(target_probs), p_row, _addr(draft_probs), q_row,
+            HPC_FP32 if target_probs.dtype == torch.float32 else HPC_BF16, _addr(uniforms), _addr(draft_lens),
+            _addr(seq_lens), Bn, T, V, _addr(out_tokens), _addr(accepted), _addr(new_lens), _addr(status))
     return out_tokens, accepted, new_lens, status
 
 
@@ -945,10 +964,9 @@ def resize_pages(block_table, old_lens, new_lens, ref_count, page_size, *, block
     ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
     moves, n_moves = _moves(moves, n_moves, Bn, dev)
     status = _status(status, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_pages_resize(_ptr(block_table), _ptr(table_out), Bn, M, int(page_size), _ptr(old_lens),
-                                     _ptr(new_lens), _ptr(ref_count), _ptr(ref_out), N, _ptr(moves), moves.shape[0],
-                                     _ptr(n_moves), _ptr(status), _stream(dev)), "hpc_pages_resize")
+    _launch("hpc_pages_resize", dev, _addr(block_table), _addr(table_out), Bn, M, int(page_size), _addr(old_lens),
+            _addr(new_lens), _addr(ref_count), _addr(ref_out), N, _addr(moves), moves.shape[0], _addr(n_moves),
+            _addr(status))
     return PageUpdate(table_out, ref_out, moves, n_moves, status)
 
 
@@ -967,11 +985,9 @@ def fork_pages(block_table, seq_lens, ref_count, parents, page_size, *, block_ta
     ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
     moves, n_moves = _moves(moves, n_moves, rows_out, dev)
     status = _status(status, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_pages_fork(_ptr(block_table), _ptr(seq_lens), rows_in, _ptr(parents), _ptr(table_out),
-                                   _ptr(lens_out), rows_out, M, int(page_size), _ptr(ref_count), _ptr(ref_out), N,
-                                   _ptr(moves), moves.shape[0], _ptr(n_moves), _ptr(status), _stream(dev)),
-               "hpc_pages_fork")
+    _launch("hpc_pages_fork", dev, _addr(block_table), _addr(seq_lens), rows_in, _addr(parents), _addr(table_out),
+            _addr(lens_out), rows_out, M, int(page_size), _addr(ref_count), _addr(ref_out), N, _addr(moves),
+            moves.shape[0], _addr(n_moves), _addr(status))
     return PageUpdate(table_out, ref_out, moves, n_moves, status, seq_lens=lens_out)
 
 
@@ -984,10 +1000,8 @@ def compact_pages(block_table, ref_count, *, block_table_out=None, ref_count_out
     page_map = _buffer(page_map, "page_map", (N,), torch.int32, dev)
     moves, n_moves = _moves(moves, n_moves, N // 2, dev)
     status = _status(status, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_pages_compact(_ptr(block_table), _ptr(table_out), Bn, M, _ptr(ref_count), _ptr(ref_out), N,
-                                      _ptr(page_map), _ptr(moves), moves.shape[0], _ptr(n_moves), _ptr(status),
-                                      _stream(dev)), "hpc_pages_compact")
+    _launch("hpc_pages_compact", dev, _addr(block_table), _addr(table_out), Bn, M, _addr(ref_count), _addr(ref_out), N,
+            _addr(page_map), _addr(moves), moves.shape[0], _addr(n_moves), _addr(status))
     return PageUpdate(table_out, ref_out, moves, n_moves, status, page_map=page_map)
 
 
@@ -1015,9 +1029,8 @@ def copy_pages(caches, moves, n_moves, *, status=None):
         raise HpcError("the caches hold no pages")
     page_bytes = caches[0][0].numel() * caches[0].element_size()
     ptrs = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
-    with torch.cuda.device(dev):
-        _check(_lib.hpc_pages_copy(ptrs, len(caches), page_bytes, num_pages, _ptr(moves), moves.shape[0],
-                                   _ptr(n_moves), _ptr(status), _stream(dev)), "hpc_pages_copy", "hpc_prompt_attention", "hpc_prompt_attention_paged")
+    _launch("hpc_pages_copy", dev, ptrs, len(caches), page_bytes, num_pages, _addr(moves), moves.shape[0],
+            _addr(n_moves), _addr(status))
     return status
 
 
