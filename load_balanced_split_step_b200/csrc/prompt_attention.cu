@@ -7,13 +7,14 @@
 // A unit of work is 256 query rows of one kv head: the group's G heads of 256 / G consecutive tokens of one
 // sequence, as two tiles A and B of 128 rows (row = G * token + head), so that a K or V block is
 // loaded once for all heads that share it. Per block of 128 keys each tile X takes two products,
-//   S_X[128 x 128] = Q_X . K^T      (tensor memory)
-//   O_X[128 x D]  += P_X . V        (P_X read from tensor memory, written over S_X)
-// with S_A, S_B, O_A, O_B filling the 512 columns of tensor memory. The tiles alternate: while the
-// tensor cores work on one, four warps run the softmax of the other, a thread per row, so that maxima and
-// sums cross no threads. The products are issued by one thread in the order P_A V, S_A', P_B V, S_B'. A new S
-// is issued only once the product that reads the P it overwrites has completed: different accumulators
-// are not ordered by the tensor pipe.
+//   S[128 x 128]  = Q_X . K^T      (tensor memory)
+//   O_X[128 x D] += P_X . V        (P_X read from tensor memory)
+// with S, P_A, P_B, O_A, O_B filling the 512 columns of tensor memory. Four warps run the softmax of a tile, a
+// thread per row, so that maxima and sums cross no threads; they hold the block's scores in registers.
+// The tiles alternate half a period apart, so that one S buffer serves both: S_B is computed while the
+// softmax of A works on the S_A it has read, and the next S_A while that of B works; neither waits for
+// a product. (With an S buffer per tile, P had to lie over S, and each S waited for the product that read that
+// P: 3700 cycles per pair of blocks, of which the softmax waited 1550. Now 2750, of which it waits 100.)
 //
 // m_i moves only when a block's maximum exceeds it by more than 8 (log2 units): p stays below 2^8, sums
 // and O are fp32, and the rescaling of O in tensor memory becomes rare. P is rounded to bf16 for its
@@ -25,9 +26,9 @@
 // at the start. The producer warp looks the units up, ahead of the others, and loads Q and
 // a ring of K and V blocks by TMA (swizzled planes of 64 elements).
 //
-// Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 one lane issues the
-// products, warp 9 looks up units and loads. A softmax thread holds the 128 scores of its row, so the
-// softmax warpgroups take registers from the third (216 + 216 + 72 = 3 x the 168 of the launch). Every
+// Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 issues the products with
+// K, warp 10 those with V, warp 9 looks up units and loads. A softmax thread holds the 128 scores of its row, so the
+// softmax warpgroups take registers from the third (208 + 208 + 88 = 3 x the 168 of the launch). Every
 // wait is bounded (2 s) and ends in HPC_DEV_TIMEOUT.
 #include <cmath>
 
@@ -37,15 +38,16 @@ namespace hpc {
 namespace {
 
 constexpr int kPaThreads = 384;
-constexpr int kPaSoftRegs = 216, kPaOtherRegs = 72;
-constexpr int kPaMmaWarp = 8, kPaLoadWarp = 9;
+constexpr int kPaSoftRegs = 208, kPaOtherRegs = 88;
+constexpr int kPaScoreWarp = 8, kPaLoadWarp = 9, kPaValueWarp = 10;
 constexpr int kPaRows = 128;            // query rows per tile
 constexpr int kPaKeys = 128;            // keys per block
 constexpr int kPaPlane = 128 * 128;     // 128 rows of 64 bf16: one swizzled plane
 constexpr int kPaBuckets = 64;
 constexpr int kPaTileRing = 2;          // units looked up ahead
-constexpr uint32_t kPaCols = 512;       // S_A 0, S_B 128, O_A 256, O_B 384
+constexpr uint32_t kPaCols = 512;       // S 0, P_A 128, P_B 192, O_A 256, O_B 384
 constexpr float kPaMove = 8.f;
+constexpr int kPaSplit = 2;               // P is handed over in two parts: after 64 keys, and whole
 constexpr int kPaStages64 = 8, kPaStages128 = 5;
 
 template <int D>
@@ -85,9 +87,9 @@ struct PaArgs {
 struct PaBars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t q_full, q_free;
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], s_read[2], p_full[2][2], pv_done[2];
   uint64_t unit_full[kPaTileRing], unit_free[kPaTileRing];
-  uint64_t drained;
+  uint64_t drained[2];
 };
 
 struct PaShared {
@@ -150,22 +152,23 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     mbar_init(bar(sh.bars.q_full), 1);
     mbar_init(bar(sh.bars.q_free), 1);
-    mbar_init(bar(sh.bars.drained), 1);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(sh.bars.drained[x]), 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(sh.bars.s_full[x]), 1);
-      mbar_init(bar(sh.bars.p_full[x]), 4);
+      mbar_init(bar(sh.bars.s_read[x]), 4);
+      for (int h = 0; h < 2; ++h) mbar_init(bar(sh.bars.p_full[x][h]), 4);
       mbar_init(bar(sh.bars.pv_done[x]), 1);
     }
     for (int t = 0; t < kPaTileRing; ++t) {
       mbar_init(bar(sh.bars.unit_full[t]), 1);
-      mbar_init(bar(sh.bars.unit_free[t]), 9);  // 8 softmax warps and the issuing thread
+      mbar_init(bar(sh.bars.unit_free[t]), 10);  // 8 softmax warps and the two that issue
     }
     fence_barrier_init();
     sh.span = 0;
     sh.bad = 0;
   }
   for (int i = threadIdx.x; i <= kPaBuckets; i += kPaThreads) sh.hist[i] = sh.rem[i] = 0;
-  if (warp == kPaMmaWarp) tmem_alloc(smem_u32(&sh.tmem), kPaCols);
+  if (warp == kPaScoreWarp) tmem_alloc(smem_u32(&sh.tmem), kPaCols);
   if (warp == kPaLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t s_at = lanes + 128 * t, o_at = lanes + 256 + 128 * t;
+    const uint32_t p_at = lanes + 128 + 64 * t, o_at = lanes + 256 + 128 * t;
     const int32_t tok = t * tokens_per_tile + row / a.group;
     const int32_t head_in = row % a.group;
     const float c = a.scale_log2;
@@ -273,8 +276,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float v[128];
-        umma::ld128(s_at, v);
-        if ((j + 1) * kPaKeys > vis_min) {
+        umma::ld128(lanes, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh.bars.s_read[t]));  // S is free for the other tile
+        const bool masked = (j + 1) * kPaKeys > vis_min;
+        if (masked) {
           const int32_t lim = vis - j * kPaKeys;
 #pragma unroll
           for (int i = 0; i < 128; ++i) v[i] = i < lim ? v[i] : -INFINITY;
@@ -303,8 +310,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             move = true;
           }
         }
+        // the product of the block before: it reads the P that is written next, and O is complete without it
+        if (done > 0) {
+          wait(sh.bars.pv_done[t], (done - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+        }
         if (__any_sync(0xffffffffu, move)) {
-          // O in tensor memory; the product of the block before has completed (this block's S waited for it)
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             float o[32];
@@ -317,22 +329,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
         const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-        float2 sum[4] = {};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float2 e = fma2(make_float2(v[64 * h + 2 * i], v[64 * h + 2 * i + 1]), c2, mc2);
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-            sum[i & 3] = add2(sum[i & 3], e);
-            w[i] = pack_bf16x2(e.x, e.y);
-          }
-          umma::st32(s_at + 32 * h, w);
-        }
-        const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l += s2.x + s2.y;
         if ((j + 1) * kPaKeys > x.keys && (t == 0 || j >= x.blocks[0])) {
           // Rows of V past the last key hold another sequence's values or what the memory held: zero, so that
           // 0 * v stays 0. The fill is the only one that its parity can mean: the stage's fill before was read
@@ -347,10 +343,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               *reinterpret_cast<uint4*>(vt + pl * kPaPlane + first * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_shared();
         }
-        umma::st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(sh.bars.p_full[t]));
+        float2 sum[4] = {};
+#pragma unroll
+        for (int h = 0; h < kPaKeys / 32; ++h) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 e = fma2(make_float2(v[32 * h + 2 * i], v[32 * h + 2 * i + 1]), c2, mc2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[i & 3] = add2(sum[i & 3], e);
+            w[i] = pack_bf16x2(e.x, e.y);
+          }
+          umma::st16(p_at + 16 * h, w);
+          if (h == kPaSplit - 1 || h == kPaKeys / 32 - 1) {  // a part of P is complete
+            umma::st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh.bars.p_full[t][h == kPaSplit - 1 ? 0 : 1]));
+          }
+        }
+        const float2 s2 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += s2.x + s2.y;
         ++done;
       }
       fill += 2 * nb_unit;
@@ -527,74 +541,96 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       if (err) atomicOr(a.status, err);
       __syncwarp();
-    } else if (warp == kPaMmaWarp) {
-      // ------------------------------------------------------------------ products
-      if (lane == 0) {
-        constexpr uint32_t kIdS = umma::idesc(128, 128, false), kIdO = umma::idesc(128, D, true);
-        uint32_t fill = 0;          // ring stages consumed (released) so far
-        uint32_t done[2] = {0, 0};  // blocks of tile A, B issued so far: phases of s_full, p_full, pv_done
-        int32_t n_q = 0;
-        auto full = [&](uint32_t f) { return wait(sh.bars.kv_full[f % L::kStages], (f / L::kStages) & 1); };
-        auto scores = [&](int t, uint32_t f) {  // S_t = Q_t . K^T of ring fill f
-          const uint32_t q = smem_u32(smem) + t * L::kTile, k = smem_u32(ring) + (f % L::kStages) * L::kTile;
-          tc_fence_after();
-  #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const int off = (kk >> 2) * kPaPlane + 32 * (kk & 3);
-            umma::mma_ss(tmem + 128 * t, umma_desc(q + off, 16, 1024, 2), umma_desc(k + off, 16, 1024, 2), kIdS, kk > 0);
-          }
-          umma_commit(bar(sh.bars.s_full[t]));
-        };
-        for (int32_t n_unit = 0;; ++n_unit) {
-          const int slot = n_unit % kPaTileRing;
-          if (!wait(sh.bars.unit_full[slot], (n_unit / kPaTileRing) & 1)) break;
-          const PaUnit x = sh.unit[slot];
-          mbar_arrive(bar(sh.bars.unit_free[slot]));
-          if (!x.valid) break;
-          const int nb = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
-          if (nb == 0) continue;
-          if (!wait(sh.bars.q_full, n_q & 1)) break;
+    } else if (warp == kPaScoreWarp || warp == kPaValueWarp) {
+      // ------------------------------------------------------------------ products (whole warp, lane 0 issues)
+      // One warp issues S = Q . K^T, another O += P . V. Issuing blocks for about as long as the product runs, so
+      // that with one warp for both every wait in between would leave the tensor cores idle.
+      const bool scores = warp == kPaScoreWarp;
+      constexpr uint32_t kIdS = umma::idesc(128, 128, false), kIdO = umma::idesc(128, D, true);
+      constexpr uint32_t kStep = L::kTile >> 4;  // a ring stage, in descriptor units
+      const uint32_t lead = lane == 0;
+      const uint64_t q_desc = umma_desc(smem_u32(smem), 16, 1024, 2);
+      const uint64_t ring_desc = umma_desc(smem_u32(ring), scores ? 16 : kPaPlane, 1024, 2);
+      int stage = scores ? 0 : 1;  // ring position of K_j (V_j): stage and phase
+      uint32_t phase = 0;
+      auto wait_all = [&](uint64_t& b, uint32_t parity) -> bool {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&b), parity));
+        if (!ok) err = HPC_DEV_TIMEOUT;
+        return ok;
+      };
+      uint32_t done[2] = {0, 0};  // products of tile A, B issued so far: phases of the tile's barriers
+      int prev = -1;              // the tile of the last S
+      int32_t n_q = 0;
+      for (int32_t n_unit = 0;; ++n_unit) {
+        const int slot = n_unit % kPaTileRing;
+        if (!wait_all(sh.bars.unit_full[slot], (n_unit / kPaTileRing) & 1)) break;
+        // the same for every lane; the exchange tells the compiler so
+        const int32_t valid = __shfl_sync(0xffffffffu, sh.unit[slot].valid, 0);
+        const int nb0 = __shfl_sync(0xffffffffu, sh.unit[slot].blocks[0], 0);
+        const int nb1 = __shfl_sync(0xffffffffu, sh.unit[slot].blocks[1], 0);
+        if (lane == 0) mbar_arrive(bar(sh.bars.unit_free[slot]));
+        __syncwarp();
+        if (!valid) break;
+        const int nb = nb0 > nb1 ? nb0 : nb1;
+        if (nb == 0) continue;
+        if (scores) {
+          if (!wait_all(sh.bars.q_full, n_q & 1)) break;
           ++n_q;
-          for (int j = 0; j <= nb && ok; ++j) {
-            // fill + 2 j is K_j, fill + 2 j - 1 is V_{j-1}
-            if (j > 0 && !full(fill + 2 * j - 1)) break;
-            if (j < nb && !full(fill + 2 * j)) break;
-            for (int t = 0; t < 2; ++t) {
-              if (j > 0 && j - 1 < x.blocks[t]) {
-                if (!wait(sh.bars.p_full[t], (done[t] - 1) & 1)) break;
-                tc_fence_after();
-                const uint32_t v = smem_u32(ring) + ((fill + 2 * j - 1) % L::kStages) * L::kTile;
-  #pragma unroll
-                for (int kk = 0; kk < kPaKeys / 16; ++kk)
-                  umma::mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, umma_desc(v + 2048 * kk, kPaPlane, 1024, 2), kIdO,
-                               (j > 1 || kk > 0) ? 1u : 0u);
-                umma_commit(bar(sh.bars.pv_done[t]));
-              }
-              if (t == 1 && j > 0) umma_commit(bar(sh.bars.kv_empty[(fill + 2 * j - 1) % L::kStages]));
-              if (j < x.blocks[t]) {
-                // the product that reads the P which this S overwrites
-                if (done[t] > 0 && !wait(sh.bars.pv_done[t], (done[t] - 1) & 1)) break;
-                scores(t, fill + 2 * j);
-                ++done[t];
-              }
-              if (t == 1 && j < nb) umma_commit(bar(sh.bars.kv_empty[(fill + 2 * j) % L::kStages]));
-            }
-            if (j == nb - 1) umma_commit(bar(sh.bars.q_free));  // the last read of Q
-          }
-          fill += 2 * nb;
         }
-        // the products in flight read shared and tensor memory
-        umma_commit(bar(sh.bars.drained));
-        if (!mbar_wait(bar(sh.bars.drained), 0)) err |= HPC_DEV_TIMEOUT;
-        if (err) atomicOr(a.status, err);
+        for (int j = 0; j < nb && ok; ++j) {
+          if (!wait_all(sh.bars.kv_full[stage], phase)) break;
+          const uint64_t at = ring_desc + static_cast<uint32_t>(stage) * kStep;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j >= (t == 0 ? nb0 : nb1)) continue;
+            if (scores) {
+              // once the softmax that the last S was for has read it
+              if (prev >= 0) wait_all(sh.bars.s_read[prev], ((prev == 0 ? done[0] : done[1]) - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * kPaPlane + 32 * (kk & 3)) >> 4;
+                umma::mma_ss(tmem, q_desc + t * kStep + off, at + off, kIdS, kk > 0, lead);
+              }
+              umma::commit(bar(sh.bars.s_full[t]), lead);
+              prev = t;
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {  // the parts of P as they come
+                wait_all(sh.bars.p_full[t][h], done[t] & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kPaKeys / 16; ++kk)
+                  if ((kk < 2 * kPaSplit) == (h == 0))
+                    umma::mma_ts(tmem + 256 + 128 * t, tmem + 128 + 64 * t + 8 * kk, at + 128 * kk, kIdO,
+                                 (j > 0 || kk > 0) ? 1u : 0u, lead);
+              }
+              umma::commit(bar(sh.bars.pv_done[t]), lead);
+            }
+            ++done[t];
+          }
+          umma::commit(bar(sh.bars.kv_empty[stage]), lead);
+          if (scores && j == nb - 1) umma::commit(bar(sh.bars.q_free), lead);  // the last read of Q
+          stage += 2;
+          if (stage >= L::kStages) {
+            stage -= L::kStages;
+            phase ^= 1;
+          }
+        }
       }
+      // the products in flight read shared and tensor memory
+      umma::commit(bar(sh.bars.drained[scores]), lead);
+      if (!mbar_wait(bar(sh.bars.drained[scores]), 0)) err |= HPC_DEV_TIMEOUT;
+      if (err && lane == 0) atomicOr(a.status, err);
       __syncwarp();
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kPaMmaWarp) {
+  if (warp == kPaScoreWarp) {
     tc_fence_after();
     tmem_free(tmem, kPaCols);
   }
