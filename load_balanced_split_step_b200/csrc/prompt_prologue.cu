@@ -8,9 +8,12 @@
 // Bound by memory: every head of a token is read once and written once or twice. A head is spread over
 // D/16 lanes: a lane holds 8 consecutive elements of each half, so that loads and stores are 16 bytes
 // wide, the rotation needs no exchange, and the mean square is reduced over D/16 lanes. A warp
-// therefore takes 512/D heads of one token at a time. It computes its token's D/2 angles itself (two per
-// lane) and never meets another warp. Where there are few tokens, the heads of one are split over
+// therefore takes 512/D heads of one token at a time, two such groups' loads in flight. It computes its token's
+// D/2 angles itself (one or two per lane) and never meets another warp; norm weights and rotation are
+// folded into four factors per pair, once per token. Where there are few tokens, the heads of one are split over
 // several warps, which each repeat the angles: up to about 8 warps per SM, latency is what counts.
+#include <type_traits>
+
 #include "hpc_common.cuh"
 
 namespace hpc {
@@ -69,98 +72,158 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPpThreads) prompt_prologue_kernel(const PpArgs a) {
-  constexpr int kLanes = D / 16;          // lanes per head
-  constexpr int kHeads = 32 / kLanes;     // heads per warp at a time
+  constexpr int kLanes = D / 16;       // lanes per head
+  constexpr int kHeads = 32 / kLanes;  // heads per warp at a time
+  constexpr int kAngles = D / 64;      // angles per lane
   __shared__ __align__(16) float s_cos[kPpWarps][D / 2];
   __shared__ __align__(16) float s_sin[kPpWarps][D / 2];
+  __shared__ __align__(16) float s_w[2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = lane % kLanes, slot_head = lane / kLanes;
+  const int sub = lane % kLanes, in_group = lane / kLanes;
   const int heads = a.Hq + 2 * a.Hkv;
-  const int64_t units = a.tokens * a.parts, stride = static_cast<int64_t>(gridDim.x) * kPpWarps;
+  double freq[kAngles];
+#pragma unroll
+  for (int k = 0; k < kAngles; ++k) freq[k] = pow(a.theta, -2.0 * (lane + 32 * k) / D);
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t w = static_cast<int64_t>(blockIdx.x) * kPpWarps + warp; w < units; w += stride) {
+  for (int k = threadIdx.x; k < D; k += kPpThreads) {
+    s_w[0][k] = a.q_w[k];
+    s_w[1][k] = a.k_w[k];
+  }
+  __syncthreads();
+  const int32_t first = a.cu[0], past = a.cu[a.batch];
+  // Each warp takes consecutive units, so that a request is looked up once for a run of its tokens.
+  const int64_t units = a.tokens * a.parts, warps = static_cast<int64_t>(gridDim.x) * kPpWarps;
+  const int64_t per = (units + warps - 1) / warps;
+  const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kPpWarps + warp) * per;
+  const int64_t w1 = w0 + per < units ? w0 + per : units;
+  const int groups_q = (a.Hq + kHeads - 1) / kHeads, groups_kv = (a.Hkv + kHeads - 1) / kHeads;
+  const int groups = groups_q + 2 * groups_kv;
+  int64_t b = 0, e = 0, L = 0;
+  int32_t r = 0;
+  for (int64_t w = w0; w < w1; ++w) {
     const int64_t i = w / a.parts;
     const int part = static_cast<int>(w - i * a.parts);
-    const int32_t first = a.cu[0], past = a.cu[a.batch];
     if (i < first || i >= past) continue;  // no request's token: left as it is
-    const int32_t r = find_request(a.cu, a.batch, i);
-    const int64_t b = a.cu[r], e = a.cu[r + 1];
-    const int64_t L = a.seq_lens[r];
+    if (i < b || i >= e) {
+      r = find_request(a.cu, a.batch, i);
+      b = a.cu[r];
+      e = a.cu[r + 1];
+      L = a.seq_lens[r];
+    }
     // what the lengths say has to hold together before anything is addressed by them
     const bool ok = b <= i && i < e && L >= e - b && L <= a.max_pages * a.P;
     const int64_t pos = ok ? L - (e - i) : 0;
     const int32_t page = ok ? a.table[r * a.max_pages + pos / a.P] : -1;
     const bool page_ok = ok && page >= 0 && page < a.num_pages;
     if (part == 0 && lane == 0 && !page_ok) atomicOr(a.status, ok ? HPC_DEV_BAD_PAGE : HPC_DEV_BAD_SEQLEN);
-    __syncwarp();
-    for (int k = lane; k < D / 2; k += 32) {
-      double sn, cs;
-      sincos(static_cast<double>(pos) * pow(a.theta, -2.0 * k / D), &sn, &cs);
-      s_cos[warp][k] = static_cast<float>(cs);
-      s_sin[warp][k] = static_cast<float>(sn);
-    }
-    __syncwarp();
     const int tok = static_cast<int>(pos % a.P);
     const __nv_bfloat16* src = a.qkv + i * heads * D + 8 * sub;
-    const int groups = (heads + kHeads - 1) / kHeads;
     const int g0 = groups * part / a.parts, g1 = groups * (part + 1) / a.parts;
-#pragma unroll 2
-    for (int g = g0; g < g1; ++g) {
-      const int h = g * kHeads + slot_head;
-      const bool live = h < heads;
-      uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
-      if (live) {
-        ra = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * D);
-        rb = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * D + D / 2);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k) {
+      double sn, cs;
+      sincos(static_cast<double>(pos) * freq[k], &sn, &cs);
+      s_cos[warp][lane + 32 * k] = static_cast<float>(cs);
+      s_sin[warp][lane + 32 * k] = static_cast<float>(sn);
+    }
+    __syncwarp();
+    // the groups [lo, hi) of one kind: q (0), k (1), v (2); two groups' loads in flight
+    auto run = [&](auto kind_c, int lo, int hi) {
+      constexpr int kind = decltype(kind_c)::value;
+      const int n = kind == 0 ? a.Hq : a.Hkv;                          // heads of the kind
+      const int h0 = kind == 0 ? 0 : (kind == 1 ? a.Hq : a.Hq + a.Hkv);  // the first one's place
+      // y1 = inv (w1 cos x1 - w2 sin x2), y2 = inv (w2 cos x2 + w1 sin x1)
+      float w1c[8], w2s[8], w2c[8], w1s[8];
+      if (kind < 2) {
+        float c[8], s[8], u1[8], u2[8];
+        load8(s_cos[warp] + 8 * sub, c);
+        load8(s_sin[warp] + 8 * sub, s);
+        load8(s_w[kind & 1] + 8 * sub, u1);
+        load8(s_w[kind & 1] + D / 2 + 8 * sub, u2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w1c[k] = u1[k] * c[k], w2s[k] = u2[k] * s[k], w2c[k] = u2[k] * c[k], w1s[k] = u1[k] * s[k];
       }
-      float x[8], y[8];
-      unpack8(ra, x);
-      unpack8(rb, y);
-      float ss = 0.f;
+      for (int g = lo; g < hi; g += 2) {
+        uint4 in[2][2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+        for (int z = 0; z < 2; ++z) {
+          const int h = (g + z) * kHeads + in_group;
+          in[z][0] = in[z][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (g + z < hi && h < n) {
+            const __nv_bfloat16* at = src + static_cast<int64_t>(h0 + h) * D;
+            in[z][0] = *reinterpret_cast<const uint4*>(at);
+            in[z][1] = *reinterpret_cast<const uint4*>(at + D / 2);
+          }
+        }
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!live) continue;
-      if (h < a.Hq + a.Hkv) {
-        const float inv = 1.f / sqrtf(ss / D + a.eps);
-        const float* wt = (h < a.Hq ? a.q_w : a.k_w) + 8 * sub;
+        for (int z = 0; z < 2; ++z) {
+          const int h = (g + z) * kHeads + in_group;
+          const bool live = g + z < hi && h < n;
+          float x[8], y[8];
+          unpack8(in[z][0], x);
+          unpack8(in[z][1], y);
+          if (kind < 2) {
+            float ss = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float c = s_cos[warp][8 * sub + k], s = s_sin[warp][8 * sub + k];
-          const float p = x[k] * inv * wt[k], q = y[k] * inv * wt[D / 2 + k];
-          x[k] = p * c - q * s;
-          y[k] = q * c + p * s;
+            for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float inv = 1.f / sqrtf(ss / D + a.eps);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float p = x[k] * inv, q = y[k] * inv;
+              x[k] = p * w1c[k] - q * w2s[k];
+              y[k] = q * w2c[k] + p * w1s[k];
+            }
+          }
+          if (live && (kind == 0 || (kind == 1 && a.k_out))) {
+            __nv_bfloat16* dst = (kind == 0 ? a.q_out + (i * a.Hq + h) * D : a.k_out + (i * a.Hkv + h) * D) + 8 * sub;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(dst) = ok ? pack8(x) : zero;
+            *reinterpret_cast<uint4*>(dst + D / 2) = ok ? pack8(y) : zero;
+          }
+          if (kind > 0 && live && page_ok) {
+            const int64_t base = (a.nhd ? (static_cast<int64_t>(page) * a.P + tok) * a.Hkv + h
+                                        : (static_cast<int64_t>(page) * a.Hkv + h) * a.P + tok) * D + 8 * sub;
+            void* pages = kind == 1 ? a.k_pages : a.v_pages;
+            if (a.fp8) {
+              const float sc = (kind == 1 ? a.k_scale : a.v_scale)[h];
+              uint8_t* dst = static_cast<uint8_t*>(pages) + base;
+              *reinterpret_cast<uint2*>(dst) = make_uint2(f32x4_to_e4m3x4(x[0] / sc, x[1] / sc, x[2] / sc, x[3] / sc),
+                                                          f32x4_to_e4m3x4(x[4] / sc, x[5] / sc, x[6] / sc, x[7] / sc));
+              *reinterpret_cast<uint2*>(dst + D / 2) =
+                  make_uint2(f32x4_to_e4m3x4(y[0] / sc, y[1] / sc, y[2] / sc, y[3] / sc),
+                             f32x4_to_e4m3x4(y[4] / sc, y[5] / sc, y[6] / sc, y[7] / sc));
+            } else {
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + base;
+              *reinterpret_cast<uint4*>(dst) = kind == 2 ? in[z][0] : pack8(x);
+              *reinterpret_cast<uint4*>(dst + D / 2) = kind == 2 ? in[z][1] : pack8(y);
+            }
+          }
         }
       }
-      const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-      const int kv = is_q ? 0 : (is_k ? h - a.Hq : h - a.Hq - a.Hkv);
-      if (is_q || (is_k && a.k_out)) {
-        __nv_bfloat16* dst = (is_q ? a.q_out + (i * a.Hq + h) * D : a.k_out + (i * a.Hkv + kv) * D) + 8 * sub;
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst) = ok ? pack8(x) : z;
-        *reinterpret_cast<uint4*>(dst + D / 2) = ok ? pack8(y) : z;
-      }
-      if (is_q || !page_ok) continue;
-      const int64_t base = (a.nhd ? (static_cast<int64_t>(page) * a.P + tok) * a.Hkv + kv
-                                  : (static_cast<int64_t>(page) * a.Hkv + kv) * a.P + tok) * D + 8 * sub;
-      void* pages = is_k ? a.k_pages : a.v_pages;
-      if (a.fp8) {
-        const float sc = (is_k ? a.k_scale : a.v_scale)[kv];
-        uint8_t* dst = static_cast<uint8_t*>(pages) + base;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(f32x4_to_e4m3x4(x[0] / sc, x[1] / sc, x[2] / sc, x[3] / sc),
-                                                    f32x4_to_e4m3x4(x[4] / sc, x[5] / sc, x[6] / sc, x[7] / sc));
-        *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(f32x4_to_e4m3x4(y[0] / sc, y[1] / sc, y[2] / sc, y[3] / sc),
-                                                            f32x4_to_e4m3x4(y[4] / sc, y[5] / sc, y[6] / sc, y[7] / sc));
-      } else {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + base;
-        *reinterpret_cast<uint4*>(dst) = pack8(x);
-        *reinterpret_cast<uint4*>(dst + D / 2) = pack8(y);
-      }
-    }
+    };
+    auto clip = [&](int lo, int n, int& x, int& y) {  // the part's share of the groups [lo, lo + n)
+      x = g0 > lo ? g0 - lo : 0;
+      y = g1 < lo + n ? g1 - lo : n;
+    };
+    int x, y;
+    clip(0, groups_q, x, y);
+    if (x < y) run(std::integral_constant<int, 0>{}, x, y);
+    clip(groups_q, groups_kv, x, y);
+    if (x < y) run(std::integral_constant<int, 1>{}, x, y);
+    clip(groups_q + groups_kv, groups_kv, x, y);
+    if (x < y) run(std::integral_constant<int, 2>{}, x, y);
   }
 }
 
@@ -219,7 +282,8 @@ extern "C" int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_
   a.nhd = kv_layout == HPC_NHD;
   a.fp8 = fp8;
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  const int groups = (num_heads + 2 * kv_heads + 512 / head_dim - 1) / (512 / head_dim);
+  const int per_group = 512 / head_dim;  // heads a warp takes at a time
+  const int groups = (num_heads + per_group - 1) / per_group + 2 * ((kv_heads + per_group - 1) / per_group);
   int64_t parts = (8 * static_cast<int64_t>(sms) + tokens - 1) / tokens;
   if (parts > groups) parts = groups;
   a.parts = static_cast<int32_t>(parts < 1 ? 1 : parts);

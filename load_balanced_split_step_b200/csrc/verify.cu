@@ -12,15 +12,19 @@
 // that only the one row that is drawn from is read: 2 V values at a rejection, V otherwise, each once
 // from HBM. A warp owns a contiguous run of the vocabulary and sums it; the sums meet in distributed
 // shared memory; the one warp whose run holds the crossing reads its run again (from L2) to find it.
+#include <type_traits>
+
 #include "hpc_common.cuh"
 
 namespace hpc {
 namespace {
 
-constexpr int kVfThreads = 512;
+constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
+constexpr int kVfRow = 32 * kVfWarps;  // a warp's run is a multiple: every warp takes an equal part of it in the search
 constexpr int kVfMaxCtas = 8;  // portable cluster
 constexpr int kVfMaxDrafts = 256;
+constexpr int kVfBatch = 16;  // entries per lane loaded together
 
 // Plain loads: an __ldg of a bf16 is an asm statement that the compiler may move ahead of the test
 // that guards it.
@@ -53,7 +57,8 @@ struct VfArgs {
 
 template <typename S>
 __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int32_t ctas) {
-  __shared__ int32_t s_first;
+  __shared__ int32_t s_lost[kVfMaxDrafts / 32];
+  __shared__ double s_sub[kVfWarps];
   __shared__ double s_warp[kVfWarps];
   __shared__ double s_cta[2][kVfMaxCtas];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -65,69 +70,80 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int3
   pdl_wait();
   pdl_launch_dependents();
 
-  int32_t n = T;
-  if (a.draft_lens) {
-    n = a.draft_lens[r];
-    if (n < 0 || n > T) {
-      if (rank == 0 && threadIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
-      n = n < 0 ? 0 : T;
-    }
-  }
-  if (threadIdx.x == 0) s_first = n;
-  __syncthreads();
+  // The kept tokens, a thread per draft; its words are loaded side by side with the count.
   const S* p_rows = static_cast<const S*>(a.p) + static_cast<int64_t>(r) * (T + 1) * a.p_stride;
   const S* q_rows = a.q ? static_cast<const S*>(a.q) + static_cast<int64_t>(r) * T * a.q_stride : nullptr;
-  if (static_cast<int32_t>(threadIdx.x) < n) {
+  const float* u_row = a.u + static_cast<int64_t>(r) * (T + 1);
+  const double u = static_cast<double>(u_row[T]);
+  int32_t n = a.draft_lens ? a.draft_lens[r] : T;
+  if (warp < kVfMaxDrafts / 32) {
     const int32_t t = threadIdx.x;
-    const int32_t x = a.drafts[static_cast<int64_t>(r) * T + t];
-    bool keep = false;
-    if (x < 0 || x >= V) {
-      if (rank == 0) atomicOr(a.status, HPC_DEV_BAD_INDEX);
-    } else {
-      const double px = vf_prob(vf_load(p_rows + t * a.p_stride + x));
-      const double qx = q_rows ? vf_prob(vf_load(q_rows + t * a.q_stride + x)) : 1.0;
-      keep = static_cast<double>(a.u[static_cast<int64_t>(r) * (T + 1) + t]) * qx < px;
+    bool keep = true;
+    if (t < T) {
+      const int32_t x = a.drafts[static_cast<int64_t>(r) * T + t];
+      const float ut = u_row[t];
+      if (x < 0 || x >= V) {
+        if (rank == 0 && t < n) atomicOr(a.status, HPC_DEV_BAD_INDEX);
+        keep = false;
+      } else {
+        const double px = vf_prob(vf_load(p_rows + t * a.p_stride + x));
+        const double qx = q_rows ? vf_prob(vf_load(q_rows + t * a.q_stride + x)) : 1.0;
+        keep = static_cast<double>(ut) * qx < px;
+      }
     }
-    if (!keep) atomicMin(&s_first, t);
+    const uint32_t lost = __ballot_sync(0xffffffffu, !keep);
+    if (lane == 0) s_lost[warp] = lost ? 32 * warp + __ffs(lost) - 1 : T;
+  }
+  if (n < 0 || n > T) {
+    if (rank == 0 && threadIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
+    n = n < 0 ? 0 : T;
   }
   __syncthreads();
-  const int32_t at = s_first;  // tokens kept; the step that is drawn
+  int32_t at = n;  // tokens kept; the step that is drawn
+#pragma unroll
+  for (int w = 0; w < kVfMaxDrafts / 32; ++w) at = min(at, s_lost[w]);
   const bool cut = at < n;
   const S* p = p_rows + at * a.p_stride;
   bool rest = cut && q_rows;
   const S* q = rest ? q_rows + at * a.q_stride : p;  // a valid row either way
   int32_t gone = cut && !q_rows ? a.drafts[static_cast<int64_t>(r) * T + at] : -1;  // one-hot draft
-  const double u = static_cast<double>(a.u[static_cast<int64_t>(r) * (T + 1) + T]);
 
   // this warp's run of the vocabulary
-  const int64_t per = (((static_cast<int64_t>(V) + ctas * kVfWarps - 1) / (ctas * kVfWarps)) + 31) & ~int64_t(31);
+  const int64_t per = (((static_cast<int64_t>(V) + ctas * kVfWarps - 1) / (ctas * kVfWarps)) + kVfRow - 1) & ~int64_t(kVfRow - 1);
   const int64_t b64 = per * (rank * kVfWarps + warp);
   const int32_t begin = static_cast<int32_t>(b64 < V ? b64 : V);
   const int32_t end = static_cast<int32_t>(b64 + per < V ? b64 + per : V);
 
-  auto weight = [&](int32_t i) -> double {
-    double w = vf_prob(vf_load(p + i));
-    if (rest) {
-      w -= vf_prob(vf_load(q + i));
-      w = w > 0.0 ? w : 0.0;
+  // The weights of entries i0 + 32 k + lane, k < kN, zero past `stop`; all loads before the first use.
+  auto load = [&](auto count, int32_t i0, int32_t stop, double* w) {
+    constexpr int kN = decltype(count)::value;
+    float x[kN], y[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int32_t i = i0 + 32 * k + lane;
+      x[k] = i < stop ? vf_load(p + i) : 0.f;
+      y[k] = rest && i < stop ? vf_load(q + i) : 0.f;
     }
-    return i == gone ? 0.0 : w;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const double d = vf_prob(x[k]) - vf_prob(y[k]);
+      w[k] = d > 0.0 && i0 + 32 * k + lane != gone ? d : 0.0;
+    }
+  };
+  auto sum_run = [&](int32_t from, int32_t stop) {  // whole warp
+    double sum = 0.0;
+    for (int32_t i = from; i < stop; i += 32 * kVfBatch) {
+      double w[kVfBatch];
+      load(std::integral_constant<int, kVfBatch>{}, i, stop, w);
+#pragma unroll
+      for (int k = 0; k < kVfBatch; ++k) sum += w[k];
+    }
+    return vf_warp_sum(sum);
   };
   double total = 0.0, before = 0.0;
   int used = 0;  // the round whose sums hold
   for (int round = 0; round < 2; ++round) {
-    double sum = 0.0;
-    if (rest) {
-#pragma unroll 8
-      for (int32_t i = begin + lane; i < end; i += 32) {
-        const double w = vf_prob(vf_load(p + i)) - vf_prob(vf_load(q + i));
-        sum += w > 0.0 ? w : 0.0;
-      }
-    } else {
-#pragma unroll 8
-      for (int32_t i = begin + lane; i < end; i += 32) sum += i == gone ? 0.0 : vf_prob(vf_load(p + i));
-    }
-    sum = vf_warp_sum(sum);
+    const double sum = sum_run(begin, end);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -183,63 +199,48 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int3
     if (chosen < 0) chosen = last;
   }
   if (chosen != rank) return;
-  int wsel = -1;
-  double base = before;
-  {
-    int wl = -1;
-    double run = before, bl = before;
+  // All warps take a part of the chosen run, and the one whose part holds the crossing looks at it 32
+  // entries at a time. (One warp alone spent 4 to 10 us here.)
+  auto choose = [&](const double* sums, double& from) {  // the part that passes the target, else the last with mass
+    int sel = -1, last_mass = -1;
+    double run = from, at_sel = from, at_last = from;
     for (int w = 0; w < kVfWarps; ++w) {
-      const double s = s_warp[w];
+      const double s = sums[w];
       if (s > 0.0) {
-        if (wsel < 0 && run + s > target) {
-          wsel = w;
-          base = run;
-        }
-        wl = w;
-        bl = run;
+        if (sel < 0 && run + s > target) sel = w, at_sel = run;
+        last_mass = w, at_last = run;
       }
       run += s;
     }
-    if (wsel < 0) {
-      wsel = wl;
-      base = bl;
-    }
-  }
-  if (warp != wsel) return;
-  // lanes own contiguous pieces of the run; then the piece, 32 entries at a time
-  const int32_t piece = static_cast<int32_t>(per >> 5);
-  double mine = 0.0;
+    from = sel >= 0 ? at_sel : at_last;
+    return sel >= 0 ? sel : last_mass;
+  };
+  double base = before;
+  const int64_t run0 = per * (rank * kVfWarps + choose(s_warp, base));
+  const int32_t part = static_cast<int32_t>(per / kVfWarps);
+  auto edge = [&](int w) { return static_cast<int32_t>(run0 + static_cast<int64_t>(part) * w < V ? run0 + static_cast<int64_t>(part) * w : V); };
   {
-    const int64_t lo = static_cast<int64_t>(begin) + static_cast<int64_t>(lane) * piece;
-#pragma unroll 8
-    for (int32_t k = 0; k < piece; ++k)
-      if (lo + k < end) mine += weight(static_cast<int32_t>(lo + k));
+    const double sum = sum_run(edge(warp), edge(warp + 1));
+    if (lane == 0) s_sub[warp] = sum;
   }
-  auto inclusive = [&](double v) {
+  __syncthreads();
+  const int sel = choose(s_sub, base);
+  if (warp != sel) return;
+  int32_t found = -1, final_mass = -1;
+  for (int32_t i0 = edge(sel); i0 < edge(sel + 1) && found < 0; i0 += 32) {
+    double w;
+    load(std::integral_constant<int, 1>{}, i0, edge(sel + 1), &w);
+    double c = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
+      const double y = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += y;
     }
-    return v;
-  };
-  const double inc = inclusive(mine);
-  const uint32_t mass = __ballot_sync(0xffffffffu, mine > 0.0);
-  uint32_t over = __ballot_sync(0xffffffffu, mine > 0.0 && base + inc > target);
-  const int lsel = over ? __ffs(over) - 1 : 31 - __clz(mass);
-  double run = base + (lsel > 0 ? __shfl_sync(0xffffffffu, inc, lsel - 1) : 0.0);
-  const int32_t lo = begin + lsel * piece;
-  const int32_t hi = lo + piece < end ? lo + piece : end;
-  int32_t found = -1, final_mass = -1;
-  for (int32_t i0 = lo; i0 < hi && found < 0; i0 += 32) {
-    const int32_t i = i0 + lane;
-    const double w = i < hi ? weight(i) : 0.0;
-    const double c = run + inclusive(w);
-    const uint32_t m = __ballot_sync(0xffffffffu, w > 0.0);
-    over = __ballot_sync(0xffffffffu, w > 0.0 && c > target);
+    const uint32_t mass = __ballot_sync(0xffffffffu, w > 0.0);
+    const uint32_t over = __ballot_sync(0xffffffffu, w > 0.0 && base + c > target);
     if (over) found = i0 + __ffs(over) - 1;
-    if (m) final_mass = i0 + 31 - __clz(m);
-    run = __shfl_sync(0xffffffffu, c, 31);
+    if (mass) final_mass = i0 + 31 - __clz(mass);
+    base += __shfl_sync(0xffffffffu, c, 31);
   }
   if (lane == 0) tokens[at] = found >= 0 ? found : final_mass;
 }
@@ -276,6 +277,7 @@ extern "C" int hpc_verify_drafts(const int32_t* draft_tokens, const void* target
   if (new_lens && !seq_lens) return fail(HPC_ERR_ARG, "new_lens needs seq_lens");
   if (prob_dtype != HPC_FP32 && prob_dtype != HPC_BF16) return fail(HPC_ERR_DTYPE, "probabilities must be FP32 or BF16");
   if (batch < 1 || max_drafts < 0 || vocab < 1) return fail(HPC_ERR_ARG, "sizes out of range");
+  if (vocab > INT32_MAX - 4096) return fail(HPC_ERR_SHAPE, "vocab too large");
   if (max_drafts > kVfMaxDrafts) return fail(HPC_ERR_SHAPE, "max_drafts above %d", kVfMaxDrafts);
   if (batch > INT32_MAX / kVfMaxCtas) return fail(HPC_ERR_SHAPE, "batch too large");
   if (target_stride < vocab || (draft_probs && draft_stride < vocab))
