@@ -8,7 +8,7 @@
 // Bound by memory: every head of a token is read once and written once or twice. A head is spread over
 // D/16 lanes: a lane holds 8 consecutive elements of each half, so that loads and stores are 16 bytes
 // wide, the rotation needs no exchange, and the mean square is reduced over D/16 lanes. A warp
-// therefore takes 512/D heads of one token at a time, two such groups' loads in flight. It computes its token's
+// therefore takes 512/D heads of one token at a time, two such groups in work and the next two on their way. It computes its token's
 // D/2 angles itself (one or two per lane) and never meets another warp; norm weights and rotation are
 // folded into four factors per pair, once per token. Where there are few tokens, the heads of one are split over
 // several warps, which each repeat the angles: up to about 8 warps per SM, latency is what counts.
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kPpThreads = 128;
 constexpr int kPpWarps = kPpThreads / 32;
+constexpr int kPpCtas = 4;  // per SM: 128 registers a thread, two groups of heads in work and two on their way
 
 struct PpArgs {
   const __nv_bfloat16* qkv;
@@ -79,7 +80,7 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPpThreads) prompt_prologue_kernel(const PpArgs a) {
+__global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(const PpArgs a) {
   constexpr int kLanes = D / 16;       // lanes per head
   constexpr int kHeads = 32 / kLanes;  // heads per warp at a time
   constexpr int kAngles = D / 64;      // angles per lane
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kPpThreads) prompt_prologue_kernel(const PpArg
       s_sin[warp][lane + 32 * k] = static_cast<float>(sn);
     }
     __syncwarp();
-    // the groups [lo, hi) of one kind: q (0), k (1), v (2); two groups' loads in flight
+    // the groups [lo, hi) of one kind: q (0), k (1), v (2)
     auto run = [&](auto kind_c, int lo, int hi) {
       constexpr int kind = decltype(kind_c)::value;
       const int n = kind == 0 ? a.Hq : a.Hkv;                          // heads of the kind
@@ -153,18 +154,22 @@ __global__ void __launch_bounds__(kPpThreads) prompt_prologue_kernel(const PpArg
 #pragma unroll
         for (int k = 0; k < 8; ++k) w1c[k] = u1[k] * c[k], w2s[k] = u2[k] * s[k], w2c[k] = u2[k] * c[k], w1s[k] = u1[k] * s[k];
       }
-      for (int g = lo; g < hi; g += 2) {
-        uint4 in[2][2];
+      uint4 in[2][2], next[2][2];
+      auto load = [&](int g, uint4 (&v)[2][2]) {
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int h = (g + z) * kHeads + in_group;
-          in[z][0] = in[z][1] = make_uint4(0u, 0u, 0u, 0u);
+          v[z][0] = v[z][1] = make_uint4(0u, 0u, 0u, 0u);
           if (g + z < hi && h < n) {
             const __nv_bfloat16* at = src + static_cast<int64_t>(h0 + h) * D;
-            in[z][0] = *reinterpret_cast<const uint4*>(at);
-            in[z][1] = *reinterpret_cast<const uint4*>(at + D / 2);
+            v[z][0] = *reinterpret_cast<const uint4*>(at);
+            v[z][1] = *reinterpret_cast<const uint4*>(at + D / 2);
           }
         }
+      };
+      load(lo, in);
+      for (int g = lo; g < hi; g += 2) {
+        load(g + 2, next);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int h = (g + z) * kHeads + in_group;
@@ -211,6 +216,8 @@ __global__ void __launch_bounds__(kPpThreads) prompt_prologue_kernel(const PpArg
             }
           }
         }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) in[z][0] = next[z][0], in[z][1] = next[z][1];
       }
     };
     auto clip = [&](int lo, int n, int& x, int& y) {  // the part's share of the groups [lo, lo + n)
@@ -288,7 +295,7 @@ extern "C" int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_
   if (parts > groups) parts = groups;
   a.parts = static_cast<int32_t>(parts < 1 ? 1 : parts);
   int64_t blocks = (tokens * a.parts + kPpWarps - 1) / kPpWarps;
-  const int64_t cap = static_cast<int64_t>(sms) * 8;
+  const int64_t cap = static_cast<int64_t>(sms) * kPpCtas;
   if (blocks > cap) blocks = cap;
   auto kern = head_dim == 128 ? prompt_prologue_kernel<128> : prompt_prologue_kernel<64>;
   const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kPpThreads), 0,
