@@ -27,9 +27,9 @@
 // a ring of K and V blocks by TMA (swizzled planes of 64 elements).
 //
 // Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 issues the products with
-// K, warp 10 those with V, warp 9 looks up units and loads. A softmax thread holds the 128 scores of its row, so the
-// softmax warpgroups take registers from the third (208 + 208 + 88 = 3 x the 168 of the launch). Every
-// wait is bounded (2 s) and ends in HPC_DEV_TIMEOUT.
+// K, warp 10 those with V, warp 9 looks up units and loads, warp 11 checks V. A softmax thread holds the 128
+// scores of its row, so the softmax warpgroups take registers from the third (208 + 208 + 88 = 3 x the 168 of the
+// launch). Every wait is bounded (2 s) and ends in HPC_DEV_TIMEOUT.
 #include <cmath>
 
 #include "umma_bf16.cuh"
@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kPaThreads = 384;
 constexpr int kPaSoftRegs = 208, kPaOtherRegs = 88;
-constexpr int kPaScoreWarp = 8, kPaLoadWarp = 9, kPaValueWarp = 10;
+constexpr int kPaScoreWarp = 8, kPaLoadWarp = 9, kPaValueWarp = 10, kPaCheckWarp = 11;
 constexpr int kPaRows = 128;            // query rows per tile
 constexpr int kPaKeys = 128;            // keys per block
 constexpr int kPaPlane = 128 * 128;     // 128 rows of 64 bf16: one swizzled plane
@@ -76,6 +76,8 @@ struct PaArgs {
   const int32_t* cu_k;      // packed
   const int32_t* table;     // paged
   const int32_t* seq_lens;  // paged
+  const __nv_bfloat16 *q, *k, *v;  // packed rows, or pages; for pa_row
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
@@ -89,12 +91,14 @@ struct PaBars {
   uint64_t q_full, q_free;
   uint64_t s_full[2], s_read[2], p_full[2][2], pv_done[2];
   uint64_t unit_full[kPaTileRing], unit_free[kPaTileRing];
+  uint64_t checked[kPaTileRing];  // per slot: the check may be a unit ahead of the epilogues
   uint64_t drained[2];
 };
 
 struct PaShared {
   PaBars bars;
   PaUnit unit[kPaTileRing];
+  int32_t found[kPaTileRing];  // the unit's partly visible blocks hold a value that is not finite
   int32_t base[kPaBuckets];   // units' token tiles in the buckets above
   int32_t count[kPaBuckets];
   int32_t hist[kPaBuckets + 1], rem[kPaBuckets + 1];
@@ -143,10 +147,61 @@ __device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, bool upper, int 
   else b = s;
 }
 
+// One row by one warp from global memory, without a product over keys that it does not see. For units whose
+// partly visible blocks of V hold infinities or NaN: there the tensor cores' 0 * v would reach rows that do not
+// see v. Such a prompt is broken; this keeps it from changing the tokens before the break.
+template <int D, bool kPaged>
+__device__ __noinline__ void pa_row(const PaArgs& a, const PaUnit& x, int32_t token, int32_t head_in, int32_t vis) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int32_t head = x.kvh * a.group + head_in;
+  const __nv_bfloat16* q = a.q + token * a.q_token + head * a.q_head;
+  float qf[kPer], o[kPer] = {};
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) qf[e] = __bfloat162float(q[lane + 32 * e]);
+  float m = -INFINITY, l = 0.f;
+  for (int32_t j = 0; j < vis; ++j) {
+    const __nv_bfloat16 *k, *v;
+    if (kPaged) {
+      int32_t page = a.table[static_cast<int64_t>(x.kv0) * a.max_pages + j / a.P];
+      if (page < 0 || page >= a.num_pages) page = 0;
+      const int64_t at = a.nhd ? (static_cast<int64_t>(page) * a.P + j % a.P) * a.Hkv + x.kvh
+                               : (static_cast<int64_t>(page) * a.Hkv + x.kvh) * a.P + j % a.P;
+      k = a.k + at * D;
+      v = a.v + at * D;
+    } else {
+      k = a.k + (x.kv0 + static_cast<int64_t>(j)) * a.k_token + x.kvh * a.k_head;
+      v = a.v + (x.kv0 + static_cast<int64_t>(j)) * a.v_token + x.kvh * a.v_head;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s = fmaf(qf[e], __bfloat162float(k[lane + 32 * e]), s);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    if (s > m) {
+      const float shrink = m == -INFINITY ? 0.f : ex2((m - s) * a.scale_log2);
+      l *= shrink;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = m == -INFINITY ? o[e] : o[e] * shrink;
+      m = s;
+    }
+    if (s == -INFINITY) continue;  // no weight
+    const float p = ex2((s - m) * a.scale_log2);
+    l += p;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = fmaf(p, __bfloat162float(v[lane + 32 * e]), o[e]);
+  }
+  const bool some = l > 0.f || l != l;
+  const int64_t at = static_cast<int64_t>(token) * a.Hq + head;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) a.out[at * D + lane + 32 * e] = __float2bfloat16_rn(some ? o[e] / l : 0.f);
+  if (a.lse && lane == 0) a.lse[at] = some ? m * a.scale + logf(l) : -INFINITY;
+}
+
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kPaThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const PaArgs a) {
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PaArgs a) {
   using L = PaLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PaShared sh;
@@ -159,7 +214,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       mbar_init(bar(sh.bars.kv_full[s]), 1);
-      mbar_init(bar(sh.bars.kv_empty[s]), 1);
+      mbar_init(bar(sh.bars.kv_empty[s]), 2);  // the products, and the check of V
     }
     mbar_init(bar(sh.bars.q_full), 1);
     mbar_init(bar(sh.bars.q_free), 1);
@@ -172,7 +227,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     for (int t = 0; t < kPaTileRing; ++t) {
       mbar_init(bar(sh.bars.unit_full[t]), 1);
-      mbar_init(bar(sh.bars.unit_free[t]), 10);  // 8 softmax warps and the two that issue
+      mbar_init(bar(sh.bars.checked[t]), 1);
+      mbar_init(bar(sh.bars.unit_free[t]), 11);  // 8 softmax warps, the two that issue, the check
     }
     fence_barrier_init();
     sh.span = 0;
@@ -270,8 +326,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const PaUnit x = sh.unit[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh.bars.unit_free[slot]));
       if (!x.valid) break;
       const int nb = t == 0 ? x.blocks[0] : x.blocks[1];
       const int nb_unit = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
@@ -384,6 +438,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+      }
+      wait(sh.bars.checked[slot], (n_unit / kPaTileRing) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const bool found = sh.found[slot] != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(sh.bars.unit_free[slot]));
+      if (found) {
+        // 0 * v is not 0 for some v that a row does not see: the rows of this tile one by one
+        for (int i = 0; i < 32; ++i) {
+          const int32_t rk = (row & ~31) + i, tk = t * tokens_per_tile + (rk >> group_shift);
+          if (x.q0 + tk < x.q_end) pa_row<D, kPaged>(a, x, x.q0 + tk, rk & (a.group - 1), min(x.vis + tk, x.keys));
+        }
+        tc_fence_before();
+        continue;
       }
       const bool some = l > 0.f || l != l;  // a NaN stays one; a row without keys is zero
       const float inv = some ? 1.f / l : 0.f;
@@ -563,6 +632,61 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       if (err) atomicOr(a.status, err);
       __syncwarp();
+    } else if (warp == kPaCheckWarp) {
+      // ------------------------------------------------------------------ values that are not finite
+      // In a block that some row of the unit sees only in part, a weight of 0 does not remove an infinity or
+      // a NaN: such blocks of V are looked through while the others work, and a unit with a find is done row by row.
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int32_t n_unit = 0;; ++n_unit) {
+        const int slot = n_unit % kPaTileRing;
+        wait(sh.bars.unit_full[slot], (n_unit / kPaTileRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int32_t valid = sh.unit[slot].valid, keys = sh.unit[slot].keys;
+        const int32_t whole = a.causal ? sh.unit[slot].vis : keys;  // keys that every row of the unit sees
+        const int nb = max(sh.unit[slot].blocks[0], sh.unit[slot].blocks[1]);
+        if (!valid) break;
+        bool found = false;
+        for (int f = 0; f < 2 * nb && ok; ++f) {
+          wait(sh.bars.kv_full[stage], phase);
+          ok = __all_sync(0xffffffffu, ok);
+          const int32_t first = (f >> 1) * kPaKeys;
+          if (ok && (f & 1) && whole < keys && first + kPaKeys > whole) {
+            const int32_t rows = keys - first < kPaKeys ? keys - first : kPaKeys;  // those past it are zeroed
+            // 0 * v added up is 0 for finite v, and a NaN from the first one that is not
+            __nv_bfloat162 sum[4] = {};
+            const __nv_bfloat162 zero = {};
+            for (int pl = 0; pl < L::kPlanes; ++pl) {
+              const uint8_t* vt = ring + stage * L::kTile + pl * kPaPlane;
+#pragma unroll 8
+              for (int i = lane; i < rows * 8; i += 32) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vt + i * 16);
+                sum[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero, sum[0]);
+                sum[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.y), zero, sum[1]);
+                sum[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.z), zero, sum[2]);
+                sum[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.w), zero, sum[3]);
+              }
+            }
+            const float2 all = __bfloat1622float2(__hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3])));
+            found |= !(all.x == 0.f) || !(all.y == 0.f);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(sh.bars.kv_empty[stage]));
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        found = __any_sync(0xffffffffu, found);
+        if (lane == 0) {
+          sh.found[slot] = found;
+          mbar_arrive(bar(sh.bars.checked[slot]));
+          mbar_arrive(bar(sh.bars.unit_free[slot]));
+        }
+      }
+      if (err && lane == 0) atomicOr(a.status, err);
     } else if (warp == kPaScoreWarp || warp == kPaValueWarp) {
       // ------------------------------------------------------------------ products (whole warp, lane 0 issues)
       // One warp issues S = Q . K^T, another O += P . V. Issuing blocks for about as long as the product runs, so
@@ -743,6 +867,9 @@ int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int6
   a.Hq = num_heads;
   a.Hkv = kv_heads;
   a.group = g;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_token = q_token_stride;
+  a.q_head = q_head_stride;
   if (tokens == 0) return HPC_OK;
   if (!aligned16(q) || !aligned16(out)) return fail(HPC_ERR_ALIGN, "q and out must be 16-byte aligned");
   if (q_token_stride % 8 || q_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0)
@@ -777,6 +904,12 @@ extern "C" int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64
     return fail(HPC_ERR_ALIGN, "strides must be multiples of 8 elements");
   a.cu_k = cu_seqlens_k ? cu_seqlens_k : cu_seqlens;
   a.kv_tokens = kv_tokens;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
   a.causal = causal != 0;
   if (kv_tokens > 0) {
     if ((rc = pa_packed_map(&mk, k, kv_tokens, kv_heads, head_dim, k_token_stride, k_head_stride, 1, kPaKeys)) != HPC_OK)
@@ -812,6 +945,8 @@ extern "C" int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride,
     return fail(HPC_ERR_SHAPE, "max_pages_per_req x page_size out of range");
   if (!aligned16(k_pages) || !aligned16(v_pages)) return fail(HPC_ERR_ALIGN, "caches must be 16-byte aligned");
   if (tokens == 0) return HPC_OK;
+  a.k = static_cast<const __nv_bfloat16*>(k_pages);
+  a.v = static_cast<const __nv_bfloat16*>(v_pages);
   a.table = block_table;
   a.seq_lens = seq_lens;
   a.max_pages = max_pages_per_req;

@@ -226,6 +226,48 @@ def test_padded_batch_is_left_alone(B):
         check(out[a:b], lse[a:b], reference(q[a:b], k[a:b], v[a:b], D ** -0.5, True))
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (2, 2, 64)])
+def test_values_that_a_query_does_not_see(B, bad, Hq, Hkv, D):
+    """A key or value that is not finite changes the queries that see it, and no other: not the earlier
+    ones in its own block of keys, not the other sequences."""
+    lens = (300, 77)
+    n = sum(lens)
+    q, k, v = draw(1, n, Hq, D), draw(2, n, Hkv, D), draw(3, n, Hkv, D)
+    clean = B.prompt_attention(q, k, v, cu(lens), return_lse=True)
+    for which, at in (("v", 40), ("v", 299), ("k", 201), ("v", 300)):
+        x = {"k": k.clone(), "v": v.clone()}
+        x[which][at, Hkv - 1, 5] = bad
+        out, lse, st = B.prompt_attention(q, x["k"], x["v"], cu(lens), return_lse=True)
+        assert int(st.item()) == 0
+        o = 0
+        for m in lens:
+            want, wl = OR.attention(q[o:o + m], x["k"][o:o + m], x["v"][o:o + m], D ** -0.5)
+            got, gl = out[o:o + m].double().cpu().numpy(), lse[o:o + m].double().cpu().numpy()
+            rows = (np.arange(m) + o < at) if o <= at < o + m else np.ones(m, bool)
+            ref = reference(q[o:o + m], k[o:o + m], v[o:o + m], D ** -0.5, True)
+            check(out[o:o + m][torch.from_numpy(rows)], lse[o:o + m][torch.from_numpy(rows)],
+                  [r[torch.from_numpy(rows)] for r in ref])
+            if which == "v":  # those that see it: the same infinities and NaN in the same places, and the rest as it was
+                assert (np.isnan(got) == np.isnan(want)).all() and (np.isinf(got) == np.isinf(want)).all()
+                assert (gl - clean[1][o:o + m].double().cpu().numpy() == 0).all() or np.allclose(gl, wl, rtol=0, atol=1e-5)
+            o += m
+
+
+def test_paged_values_that_a_query_does_not_see(B):
+    lens, ctx = (200,), (150,)
+    for layout in ("HND", "NHD"):
+        kp, vp, table, seq, ks, vs = paged(5, lens, ctx, 1, 128, 64, layout)
+        q = draw(3, 200, 8, 128)
+        clean, _, _ = B.prompt_attention_paged(q, kp, vp, table, seq, cu(lens), kv_layout=layout)
+        page = int(table[0, 240 // 64])
+        (vp[page, 0, 240 % 64] if layout == "HND" else vp[page, 240 % 64, 0])[9] = math.nan  # key 240: query 90
+        out, _, st = B.prompt_attention_paged(q, kp, vp, table, seq, cu(lens), kv_layout=layout)
+        assert int(st.item()) == 0
+        check(out[:90], None, [r[:90] for r in reference(q, ks[0], vs[0], 128 ** -0.5, True)])
+        assert torch.isnan(out[90:, :, 9]).all() and not torch.isnan(out[:, :, :9]).any()
+
+
 def test_strides(B):
     """Heads and tokens apart, and a layout with the heads outermost."""
     n, Hq, Hkv, D = 200, 4, 2, 64
