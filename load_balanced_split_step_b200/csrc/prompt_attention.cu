@@ -44,7 +44,7 @@ constexpr int kPaRows = 128;            // query rows per tile
 constexpr int kPaKeys = 128;            // keys per block
 constexpr int kPaPlane = 128 * 128;     // 128 rows of 64 bf16: one swizzled plane
 constexpr int kPaBuckets = 64;
-constexpr int kPaTileRing = 2;          // units looked up ahead
+constexpr int kPaTileRing = 3;          // units looked up ahead
 constexpr uint32_t kPaCols = 512;       // S 0, P_A 128, P_B 192, O_A 256, O_B 384
 constexpr float kPaMove = 8.f;
 constexpr int kPaSplit = 2;               // P is handed over in two parts: after 64 keys, and whole
