@@ -713,9 +713,21 @@ def gather_pages(block_table, req, col0, width=None, out=None, status=None):
     return out
 
 
+def _want(t, name, dtype, dev):
+    """``_need`` with its common outcome first: these calls are a few microseconds long."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.device == dev and t.is_contiguous()):
+        _need(t, name, dtype, dev)
+
+
+def _empty(shape, dtype, dev):
+    n = len(shape)
+    strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+
+
 def _packed(cu_seqlens, dev, batch=None):
     """Checks the boundaries of packed prompts; returns the number of requests."""
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, dev)
     n = cu_seqlens.numel() - 1
     if cu_seqlens.dim() != 1 or n < 1 or (batch is not None and n != batch):
         raise HpcError("cu_seqlens must be [batch + 1]" + ("" if batch is None else f" for a batch of {batch}"))
@@ -730,11 +742,11 @@ _words = {}  # (device, stream) -> status words zeroed there and not handed out 
 
 
 def _status(status, dev):
-    """The caller's status word, or a zeroed one. Words are zeroed 64 at a time on the stream that will use
+    """The caller's status word, or a zeroed one. Words are zeroed 128 at a time on the stream that will use
     them: a memset of its own for each call costs as much as a small kernel. A captured call zeroes its
     own word, at every replay."""
     if status is not None:
-        _need(status, "status", torch.int32, dev)
+        _want(status, "status", torch.int32, dev)
         return status
     if torch.cuda.is_current_stream_capturing():
         return new_status(dev)
@@ -742,26 +754,28 @@ def _status(status, dev):
     try:
         return words.pop()
     except IndexError:
-        words.extend(torch.zeros(64, dtype=torch.int32, device=dev).split(1))
+        words.extend(torch.zeros(128, dtype=torch.int32, device=dev).split(1))
         return words.pop()
 
 
 def _launch(name, dev, *args):
     """Calls a library function that ends in a stream, on the current stream of the tensors' device."""
+    fn, stream = getattr(_lib, name), torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        rc = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
-    _check(rc, name)
+            rc = fn(*args, stream)
+    if rc != HPC_OK:
+        _check(rc, name)
 
 
 def _buffer(t, name, shape, dtype, dev):
     """An output the caller may hand in."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
+        return _empty(shape, dtype, dev)
+    _want(t, name, dtype, dev)
+    if t.shape != shape:
         raise HpcError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -775,8 +789,8 @@ def prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block
     request are left as they were."""
     _need(qkv, "qkv", torch.bfloat16)
     dev = qkv.device
-    _need(q_norm_w, "q_norm_w", torch.float32, dev)
-    _need(k_norm_w, "k_norm_w", torch.float32, dev)
+    _want(q_norm_w, "q_norm_w", torch.float32, dev)
+    _want(k_norm_w, "k_norm_w", torch.float32, dev)
     if qkv.dim() != 3 or qkv.shape[1] != num_heads + 2 * kv_heads:
         raise HpcError("qkv must be [tokens, num_heads + 2*kv_heads, head_dim]")
     n, _, D = qkv.shape
@@ -896,12 +910,12 @@ def verify_drafts(draft_tokens, target_probs, draft_probs, uniforms, *, draft_le
     q_row = V
     if draft_probs is not None:
         q_row = _rows(draft_probs, "draft_probs", (Bn, T, V), target_probs.dtype, dev)
-    _need(uniforms, "uniforms", torch.float32, dev)
+    _want(uniforms, "uniforms", torch.float32, dev)
     if tuple(uniforms.shape) != (Bn, T + 1):
         raise HpcError(f"uniforms must be [{Bn}, {T + 1}]")
     for name, t in (("draft_lens", draft_lens), ("seq_lens", seq_lens)):
         if t is not None:
-            _need(t, name, torch.int32, dev)
+            _want(t, name, torch.int32, dev)
             if t.numel() != Bn:
                 raise HpcError(f"{name} must be [batch]")
     out_tokens = _buffer(out_tokens, "out_tokens", (Bn, T + 1), torch.int32, dev)
@@ -935,7 +949,7 @@ def _pool(block_table, ref_count):
     """(device, rows, max_pages, num_pages) of a cache's table and reference counts."""
     _need(block_table, "block_table", torch.int32)
     dev = block_table.device
-    _need(ref_count, "ref_count", torch.int32, dev)
+    _want(ref_count, "ref_count", torch.int32, dev)
     if block_table.dim() != 2 or ref_count.dim() != 1:
         raise HpcError("block_table must be [rows, max_pages] and ref_count [num_pages]")
     return dev, block_table.shape[0], block_table.shape[1], ref_count.numel()
@@ -943,8 +957,8 @@ def _pool(block_table, ref_count):
 
 def _moves(moves, n_moves, capacity, dev):
     if moves is None:
-        moves = torch.empty((max(capacity, 1), 2), dtype=torch.int32, device=dev)
-    _need(moves, "moves", torch.int32, dev)
+        moves = _empty((max(capacity, 1), 2), torch.int32, dev)
+    _want(moves, "moves", torch.int32, dev)
     if moves.dim() != 2 or moves.shape[1] != 2:
         raise HpcError("moves must be [capacity, 2]")
     return moves, _buffer(n_moves, "n_moves", (1,), torch.int32, dev)
@@ -957,7 +971,7 @@ def resize_pages(block_table, old_lens, new_lens, ref_count, page_size, *, block
     table and new counts; handing the inputs in as outputs updates them in place."""
     dev, Bn, M, N = _pool(block_table, ref_count)
     for name, t in (("old_lens", old_lens), ("new_lens", new_lens)):
-        _need(t, name, torch.int32, dev)
+        _want(t, name, torch.int32, dev)
         if t.numel() != Bn:
             raise HpcError(f"{name} must be [batch]")
     table_out = _buffer(block_table_out, "block_table_out", (Bn, M), torch.int32, dev)
@@ -975,10 +989,10 @@ def fork_pages(block_table, seq_lens, ref_count, parents, page_size, *, block_ta
     """New row r is old row parents[r], -1 for none (``hpc_pages_fork``): full pages are shared, a
     part-filled last page is copied for every child but the first, rows without children are released."""
     dev, rows_in, M, N = _pool(block_table, ref_count)
-    _need(seq_lens, "seq_lens", torch.int32, dev)
+    _want(seq_lens, "seq_lens", torch.int32, dev)
     if seq_lens.numel() != rows_in:
         raise HpcError("seq_lens must be [rows]")
-    _need(parents, "parents", torch.int32, dev)
+    _want(parents, "parents", torch.int32, dev)
     rows_out = parents.numel()
     table_out = _buffer(block_table_out, "block_table_out", (rows_out, M), torch.int32, dev)
     lens_out = _buffer(seq_lens_out, "seq_lens_out", (rows_out,), torch.int32, dev)
@@ -1014,7 +1028,7 @@ def copy_pages(caches, moves, n_moves, *, status=None):
     dev = moves.device
     if moves.dim() != 2 or moves.shape[1] != 2:
         raise HpcError("moves must be [capacity, 2]")
-    _need(n_moves, "n_moves", torch.int32, dev)
+    _want(n_moves, "n_moves", torch.int32, dev)
     if n_moves.numel() != 1:
         raise HpcError("n_moves must hold one count")
     status = _status(status, dev)
