@@ -209,7 +209,26 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
+  // The entries that stay, and -1 past them; the new ones are written below by whoever holds the page. A new
+  // table is written now, under the latencies of the first phases, and an old one once nothing can fail.
+  auto keep_entries = [&]() {
+    for (int32_t r = gw; r < rows; r += kPgAllWarps) {
+      const int64_t o = a.lens[r], n = a.want[r];
+      const bool ok = len_ok(a, o) && len_ok(a, n);
+      const int32_t from = ok ? held(a, o) : M, to = ok ? held(a, n) : M;
+      const int32_t keep = from < to ? from : to;
+      const int32_t* in = a.table_in + static_cast<int64_t>(r) * M;
+      int32_t* out = a.table_out + static_cast<int64_t>(r) * M;
+      if (in != out) {
+#pragma unroll 4
+        for (int32_t j = lane; j < keep; j += 32) out[j] = in[j];
+      }
+#pragma unroll 4
+      for (int32_t j = to + lane; j < M; j += 32) out[j] = -1;
+    }
+  };
   copy_counts(a.ref_in, a.ref_out, a.num_pages, gtid);
+  if (a.table_in != a.table_out) keep_entries();
   cluster_sync();
   // releases; `sign` +1 takes them back
   auto release = [&](int32_t sign) {
@@ -259,23 +278,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
       for (int64_t i = gtid; i < static_cast<int64_t>(rows) * M; i += kPgCtas * kPgThreads) a.table_out[i] = a.table_in[i];
     return;
   }
-  // the entries that stay, and -1 past them; the new ones are written below by whoever holds the page
-  for (int32_t r = gw; r < rows; r += kPgAllWarps) {
-    const int64_t o = a.lens[r], n = a.want[r];
-    const bool ok = len_ok(a, o) && len_ok(a, n);
-    const int32_t from = ok ? held(a, o) : M, to = ok ? held(a, n) : M;
-    const int32_t keep = from < to ? from : to;
-    const bool cow = (r + 1 < rows ? s_cow[r + 1] : copies) != s_cow[r];
-    const int32_t at = cow ? static_cast<int32_t>(o / P) : -1;
-    for (int32_t j = lane; j < M; j += 32) {
-      const int64_t i = static_cast<int64_t>(r) * M + j;
-      if (j < keep) {
-        if (j != at && a.table_in != a.table_out) a.table_out[i] = a.table_in[i];
-      } else if (j >= to) {
-        a.table_out[i] = -1;
-      }
-    }
-  }
+  if (a.table_in == a.table_out) keep_entries();
   warp_visit(a.ref_out, begin, end, before, total, is_free, [&](int32_t p, int32_t k) {
     const int32_t r = prefix_find(s_need, rows, k);
     const int64_t o = a.lens[r];
@@ -284,7 +287,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     const bool copy = cow && nth == 0;
     const int32_t j = copy ? static_cast<int32_t>(o / P) : held(a, o) + nth - (cow ? 1 : 0);
     const int64_t i = static_cast<int64_t>(r) * M + j;
-    if (copy) a.moves[s_cow[r]] = make_int2(a.table_in[i], p);
+    if (copy) a.moves[s_cow[r]] = make_int2(a.table_in[i], p);  // the entry itself is this thread's
     a.table_out[i] = p;
     a.ref_out[p] = 1;
   });
@@ -346,6 +349,23 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     s_need[r] = n % P != 0 && s_first[f] != r ? 1 : 0;
   }
   const int32_t total = block_prefix(s_need, rows, sh.red);
+  // The rows, but for the pages that are copied: those are written below by whoever holds the new page.
+  auto write_rows = [&](bool filled) {
+    for (int32_t r = gw; r < rows; r += kPgAllWarps) {
+      int32_t f = 0;
+      const int64_t n = filled ? length(r, f) : 0;
+      if (lane == 0) a.lens_out[r] = static_cast<int32_t>(n);
+      const int32_t np = held(a, n);
+      const bool fresh = (r + 1 < rows ? s_need[r + 1] : total) != s_need[r];
+      const int32_t* in = a.table_in + static_cast<int64_t>(f < 0 ? 0 : f) * M;
+      int32_t* out = a.table_out + static_cast<int64_t>(r) * M;
+#pragma unroll 4
+      for (int32_t j = lane; j < np - (fresh ? 1 : 0); j += 32) out[j] = in[j];
+#pragma unroll 4
+      for (int32_t j = np + lane; j < M; j += 32) out[j] = -1;
+    }
+  };
+  write_rows(true);
   cluster_sync();  // the counts are copied
   // One change of count per held entry of an old row: its children less itself. Of a part-filled last
   // page one child keeps the reference and the others leave.
@@ -377,22 +397,11 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     *a.n_moves = fits ? total : 0;
     if (!fits) atomicOr(a.status, HPC_DEV_CAPACITY);
   }
-  if (!fits) recount(-1);  // too few pages: the counts as they were, and empty rows
-  for (int32_t r = gw; r < rows; r += kPgAllWarps) {
-    int32_t f;
-    const int64_t n = fits ? length(r, f) : 0;
-    if (lane == 0) a.lens_out[r] = static_cast<int32_t>(n);
-    const int32_t np = held(a, n);
-    const bool fresh = (r + 1 < rows ? s_need[r + 1] : total) != s_need[r];
-    for (int32_t j = lane; j < M; j += 32) {
-      if (j < np) {
-        if (!fresh || j != np - 1) a.table_out[static_cast<int64_t>(r) * M + j] = a.table_in[static_cast<int64_t>(f) * M + j];
-      } else {
-        a.table_out[static_cast<int64_t>(r) * M + j] = -1;
-      }
-    }
+  if (!fits) {
+    recount(-1);  // too few pages: the counts as they were, and empty rows
+    write_rows(false);
+    return;
   }
-  if (!fits) return;
   warp_visit(a.ref_out, begin, end, before, total, is_free, [&](int32_t p, int32_t k) {
     const int32_t r = prefix_find(s_need, rows, k);
     int32_t f;

@@ -12,6 +12,7 @@
 // D/2 angles itself (one or two per lane) and never meets another warp; norm weights and rotation are
 // folded into four factors per pair, once per token. Where there are few tokens, the heads of one are split over
 // several warps, which each repeat the angles: up to about 8 warps per SM, latency is what counts.
+#include <cmath>
 #include <type_traits>
 
 #include "hpc_common.cuh"
@@ -38,7 +39,7 @@ struct PpArgs {
   const int32_t* table;
   uint32_t* status;
   int64_t tokens, max_pages;
-  double theta;
+  double log2_theta;
   float eps;
   int32_t batch, Hq, Hkv, num_pages, P, nhd, fp8, parts;
 };
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(co
   const int heads = a.Hq + 2 * a.Hkv;
   double freq[kAngles];
 #pragma unroll
-  for (int k = 0; k < kAngles; ++k) freq[k] = pow(a.theta, -2.0 * (lane + 32 * k) / D);
+  for (int k = 0; k < kAngles; ++k) freq[k] = exp2(-2.0 * (lane + 32 * k) / D * a.log2_theta);
   pdl_wait();
   pdl_launch_dependents();
   for (int k = threadIdx.x; k < D; k += kPpThreads) {
@@ -279,7 +280,7 @@ extern "C" int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_
   a.status = status;
   a.tokens = tokens;
   a.max_pages = max_pages_per_req;
-  a.theta = static_cast<double>(rope_theta);
+  a.log2_theta = std::log2(static_cast<double>(rope_theta));
   a.eps = eps;
   a.batch = batch;
   a.Hq = num_heads;
