@@ -8,10 +8,14 @@
 // samples. Everything is compared and summed in fp64 (u q is exact there, and so is p - q for most
 // pairs of floats), so that the choice next to a border does not hang on the order of a sum.
 //
-// One cluster of CTAs per request. Each CTA decides the kept tokens on its own (a few words), so
+// One cluster of up to 8 CTAs per request. Each CTA decides the kept tokens on its own (a few words), so
 // that only the one row that is drawn from is read: 2 V values at a rejection, V otherwise, each once
 // from HBM. A warp owns a contiguous run of the vocabulary and sums it; the sums meet in distributed
-// shared memory; the one warp whose run holds the crossing reads its run again (from L2) to find it.
+// shared memory; the CTA whose run holds the crossing reads it again (from L2) to find it.
+//
+// Bound by the row streams and, close behind, by the conversions to fp64 (one per value, 16 lanes per cycle and
+// SM). 64 requests, vocabulary 131071, fp32: 16.8 us with the launch, 4.0 TB/s; 25 us with every value tested
+// in fp64, 39 us with one warp searching the run. One request of 32000: 6.4 us, latencies.
 #include <type_traits>
 
 #include "hpc_common.cuh"
@@ -19,12 +23,12 @@
 namespace hpc {
 namespace {
 
-constexpr int kVfThreads = 256;
+constexpr int kVfThreads = 512;
 constexpr int kVfWarps = kVfThreads / 32;
-constexpr int kVfRow = 32 * kVfWarps;  // a warp's run is a multiple: every warp takes an equal part of it in the search
 constexpr int kVfMaxCtas = 8;  // portable cluster
 constexpr int kVfMaxDrafts = 256;
-constexpr int kVfBatch = 16;  // entries per lane loaded together
+constexpr int kVfBatch = 8;   // entries per lane loaded together
+constexpr int kVfRows = 4;    // rows of 32 entries looked at together in the end
 
 // Plain loads: an __ldg of a bf16 is an asm statement that the compiler may move ahead of the test
 // that guards it.
@@ -38,6 +42,33 @@ __device__ __forceinline__ double vf_warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Inclusive prefix over the lanes.
+__device__ __forceinline__ double vf_scan(double v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// The part (of n <= 32, in order) in which the running sum passes the target, or the last with any mass;
+// `from` is the sum before the parts and becomes the sum before the chosen one. Whole warp, mass somewhere.
+// Sums of parts can round differently from the part's own sums, so that "passes" may find no entry inside; the
+// last with mass is then the entry up to that rounding. A target that nothing passes (u >= 1, NaN) ends
+// there too.
+__device__ __forceinline__ int vf_choose(const double* sums, int n, double target, double& from) {
+  const int lane = threadIdx.x & 31;
+  const double s = lane < n ? sums[lane] : 0.0, inc = vf_scan(s);
+  const uint32_t over = __ballot_sync(0xffffffffu, s > 0.0 && from + inc > target);
+  const uint32_t mass = __ballot_sync(0xffffffffu, s > 0.0);
+  const int sel = over ? __ffs(over) - 1 : 31 - __clz(mass);
+  const double before = __shfl_sync(0xffffffffu, inc, sel > 0 ? sel - 1 : 0);
+  from += sel > 0 ? before : 0.0;
+  return sel;
 }
 
 struct VfArgs {
@@ -56,11 +87,11 @@ struct VfArgs {
 };
 
 template <typename S>
-__global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int32_t ctas) {
+__global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VfArgs a, int32_t ctas) {
   __shared__ int32_t s_lost[kVfMaxDrafts / 32];
   __shared__ double s_sub[kVfWarps];
   __shared__ double s_warp[kVfWarps];
-  __shared__ double s_cta[2][kVfMaxCtas];
+  __shared__ double s_cta[3][kVfMaxCtas];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t r = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   const int32_t T = a.T, V = a.V;
@@ -109,7 +140,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int3
   int32_t gone = cut && !q_rows ? a.drafts[static_cast<int64_t>(r) * T + at] : -1;  // one-hot draft
 
   // this warp's run of the vocabulary
-  const int64_t per = (((static_cast<int64_t>(V) + ctas * kVfWarps - 1) / (ctas * kVfWarps)) + kVfRow - 1) & ~int64_t(kVfRow - 1);
+  const int64_t per = (((static_cast<int64_t>(V) + ctas * kVfWarps - 1) / (ctas * kVfWarps)) + 31) & ~int64_t(31);
   const int64_t b64 = per * (rank * kVfWarps + warp);
   const int32_t begin = static_cast<int32_t>(b64 < V ? b64 : V);
   const int32_t end = static_cast<int32_t>(b64 + per < V ? b64 + per : V);
@@ -130,19 +161,50 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int3
       w[k] = d > 0.0 && i0 + 32 * k + lane != gone ? d : 0.0;
     }
   };
-  auto sum_run = [&](int32_t from, int32_t stop) {  // whole warp
+  // Sum of the weights of [from, stop) (whole warp). Conversions to fp64 and the instructions around them bound
+  // this as much as memory does, so whole batches go without tests: fmaxf makes NaN and negative values 0, and
+  // an infinity shows in the sum. Then (`careful`) every value is tested.
+  bool careful = false;
+  auto sum_run = [&](int32_t from, int32_t stop) {
     double sum = 0.0;
-    for (int32_t i = from; i < stop; i += 32 * kVfBatch) {
-      double w[kVfBatch];
-      load(std::integral_constant<int, kVfBatch>{}, i, stop, w);
+    int32_t i = from;
+    if (!careful && gone < 0) {
+      if (rest) {
+        for (; i + 32 * kVfBatch <= stop; i += 32 * kVfBatch) {
+          float x[kVfBatch], y[kVfBatch];
 #pragma unroll
-      for (int k = 0; k < kVfBatch; ++k) sum += w[k];
+          for (int k = 0; k < kVfBatch; ++k) {
+            x[k] = vf_load(p + i + lane + 32 * k);
+            y[k] = vf_load(q + i + lane + 32 * k);
+          }
+#pragma unroll
+          for (int k = 0; k < kVfBatch; ++k) {
+            const float a = fmaxf(x[k], 0.f), b = fmaxf(y[k], 0.f);
+            const double d = static_cast<double>(a) - static_cast<double>(b);
+            if (a > b) sum += d;
+          }
+        }
+      } else {
+        for (; i + 32 * kVfBatch <= stop; i += 32 * kVfBatch) {
+          float x[kVfBatch];
+#pragma unroll
+          for (int k = 0; k < kVfBatch; ++k) x[k] = vf_load(p + i + lane + 32 * k);
+#pragma unroll
+          for (int k = 0; k < kVfBatch; ++k) sum += static_cast<double>(fmaxf(x[k], 0.f));
+        }
+      }
+    }
+    for (; i < stop; i += 32 * kVfRows) {
+      double w[kVfRows];
+      load(std::integral_constant<int, kVfRows>{}, i, stop, w);
+#pragma unroll
+      for (int k = 0; k < kVfRows; ++k) sum += w[k];
     }
     return vf_warp_sum(sum);
   };
-  double total = 0.0, before = 0.0;
+  double total = 0.0;
   int used = 0;  // the round whose sums hold
-  for (int round = 0; round < 2; ++round) {
+  for (int round = 0; round < 3; ++round) {
     const double sum = sum_run(begin, end);
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
@@ -156,17 +218,18 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int3
     }
     // not the .aligned forms: nothing holds a warp together after the branch above
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-    total = 0.0;
     used = round;
-    for (int c = 0; c < ctas; ++c) {
-      if (c == rank) before = total;
-      total += s_cta[round][c];
-    }
-    if (total > 0.0 || (!rest && gone < 0)) break;  // the same in every CTA
-    // The rest has no mass (the target gives nothing outside the draft's share): the target's own row.
+    total = __shfl_sync(0xffffffffu, vf_scan(lane < ctas ? s_cta[round][lane] : 0.0), ctas - 1);
+    const bool finite = total <= 1.7976931348623157e308;  // the same in every CTA, as all that follows
+    if (finite && (total > 0.0 || (!rest && gone < 0))) break;
     __syncthreads();
-    rest = false;
-    gone = -1;
+    if (!finite) {
+      careful = true;
+    } else {
+      // The rest has no mass (the target gives nothing outside the draft's share): the target's own row.
+      rest = false;
+      gone = -1;
+    }
   }
 
   int32_t* tokens = a.tokens + static_cast<int64_t>(r) * (T + 1);
@@ -182,65 +245,36 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(const VfArgs a, int3
   }
   if (!(total > 0.0)) return;
 
-  // The CTA, then the warp, then the entry at which the running sum passes the target. Sums by part
-  // can round differently from the sums of the parts; where no part of the chosen one passes, the last with
-  // any mass is taken, which is the same entry up to that rounding. A u of 1 or more (or NaN)
-  // takes the last entry with mass.
+  // The CTA, then the warp's run, then the part of the run, then the entry at which the running sum passes
   const double target = u * total;
-  int chosen = -1, last = -1;
-  {
-    double run = 0.0;
-    for (int c = 0; c < ctas; ++c) {
-      const double s = s_cta[used][c];
-      run += s;
-      if (s > 0.0) last = c;
-      if (chosen < 0 && s > 0.0 && run > target) chosen = c;
-    }
-    if (chosen < 0) chosen = last;
-  }
-  if (chosen != rank) return;
+  double base = 0.0;
+  if (vf_choose(s_cta[used], ctas, target, base) != rank) return;
   // All warps take a part of the chosen run, and the one whose part holds the crossing looks at it 32
   // entries at a time. (One warp alone spent 4 to 10 us here.)
-  auto choose = [&](const double* sums, double& from) {  // the part that passes the target, else the last with mass
-    int sel = -1, last_mass = -1;
-    double run = from, at_sel = from, at_last = from;
-    for (int w = 0; w < kVfWarps; ++w) {
-      const double s = sums[w];
-      if (s > 0.0) {
-        if (sel < 0 && run + s > target) sel = w, at_sel = run;
-        last_mass = w, at_last = run;
-      }
-      run += s;
-    }
-    from = sel >= 0 ? at_sel : at_last;
-    return sel >= 0 ? sel : last_mass;
-  };
-  double base = before;
-  const int64_t run0 = per * (rank * kVfWarps + choose(s_warp, base));
-  const int32_t part = static_cast<int32_t>(per / kVfWarps);
-  auto edge = [&](int w) { return static_cast<int32_t>(run0 + static_cast<int64_t>(part) * w < V ? run0 + static_cast<int64_t>(part) * w : V); };
+  const int64_t run0 = per * (rank * kVfWarps + vf_choose(s_warp, kVfWarps, target, base));
+  const int64_t run1 = run0 + per < V ? run0 + per : V, part = ((per + kVfWarps - 1) / kVfWarps + 31) & ~int64_t(31);
+  auto edge = [&](int w) { return static_cast<int32_t>(run0 + part * w < run1 ? run0 + part * w : run1); };
   {
     const double sum = sum_run(edge(warp), edge(warp + 1));
     if (lane == 0) s_sub[warp] = sum;
   }
   __syncthreads();
-  const int sel = choose(s_sub, base);
+  const int sel = vf_choose(s_sub, kVfWarps, target, base);
   if (warp != sel) return;
   int32_t found = -1, final_mass = -1;
-  for (int32_t i0 = edge(sel); i0 < edge(sel + 1) && found < 0; i0 += 32) {
-    double w;
-    load(std::integral_constant<int, 1>{}, i0, edge(sel + 1), &w);
-    double c = w;
+  for (int32_t i0 = edge(sel); i0 < edge(sel + 1) && found < 0; i0 += 32 * kVfRows) {
+    double rows[kVfRows];
+    load(std::integral_constant<int, kVfRows>{}, i0, edge(sel + 1), rows);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += y;
+    for (int k = 0; k < kVfRows; ++k) {
+      const double w = rows[k];
+      const double c = vf_scan(w);
+      const uint32_t mass = __ballot_sync(0xffffffffu, w > 0.0);
+      const uint32_t over = __ballot_sync(0xffffffffu, w > 0.0 && base + c > target);
+      if (over && found < 0) found = i0 + 32 * k + __ffs(over) - 1;
+      if (mass) final_mass = i0 + 32 * k + 31 - __clz(mass);
+      base += __shfl_sync(0xffffffffu, c, 31);
     }
-    const uint32_t mass = __ballot_sync(0xffffffffu, w > 0.0);
-    const uint32_t over = __ballot_sync(0xffffffffu, w > 0.0 && base + c > target);
-    if (over) found = i0 + __ffs(over) - 1;
-    if (mass) final_mass = i0 + 31 - __clz(mass);
-    base += __shfl_sync(0xffffffffu, c, 31);
   }
   if (lane == 0) tokens[at] = found >= 0 ? found : final_mass;
 }
@@ -298,8 +332,13 @@ extern "C" int hpc_verify_drafts(const int32_t* draft_tokens, const void* target
   a.T = max_drafts;
   a.V = vocab;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = prob_dtype == HPC_FP32 ? launch_verify<float>(a, batch, kVfMaxCtas, st)
-                                               : launch_verify<__nv_bfloat16>(a, batch, kVfMaxCtas, st);
+  // As many CTAs per request (a power of two, at most 8) as are on the GPU at once, two per SM: those of a
+  // second wave would start only when the first has streamed its rows.
+  const int64_t room = 2 * static_cast<int64_t>(device_sm_count() > 0 ? device_sm_count() : 148);
+  int32_t ctas = kVfMaxCtas;
+  while (ctas > 1 && static_cast<int64_t>(batch) * ctas > room) ctas /= 2;
+  const cudaError_t e = prob_dtype == HPC_FP32 ? launch_verify<float>(a, batch, ctas, st)
+                                               : launch_verify<__nv_bfloat16>(a, batch, ctas, st);
   if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "verify_kernel: %s", cudaGetErrorString(e));
   return check_launch("verify_kernel");
 }

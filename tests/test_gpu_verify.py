@@ -101,11 +101,13 @@ def test_rest_without_mass_takes_the_target(B):
     assert tokens[0].tolist() == [9, -1]
 
 
-def test_values_that_are_no_probabilities_count_as_zero(B):
-    x, p, q, u, n, lens = case(77, 8, 2, 999, torch.float32)
-    for bad, at in ((float("nan"), 3), (float("inf"), 500), (-1.0, 998), (float("-inf"), 0)):
-        p[:, :, at] = bad
-        q[:, :, (at + 1) % 999] = bad
+@pytest.mark.parametrize("V", [999, 40001, 131072])
+@pytest.mark.parametrize("bads", [("nan", "inf", -1.0, "-inf"), ("nan", -1.0)])
+def test_values_that_are_no_probabilities_count_as_zero(B, V, bads):
+    x, p, q, u, n, lens = case(77, 4, 2, V, torch.float32)
+    for bad, at in zip(bads, (3, V // 2, V - 1, 0)):
+        p[:, :, at] = float(bad)
+        q[:, :, (at + 1) % V] = float(bad)
     check(B, x, p, q, u, n, lens)
     u[:, -1] = float("nan")  # no sum passes a NaN: the last entry with mass
     check(B, x, p, q, u, n, lens)
