@@ -804,10 +804,10 @@ def prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block
     q_out = _buffer(q_out, "q_out", (n, num_heads, D), torch.bfloat16, dev)
     k_out = _buffer(k_out, "k_out", (n, kv_heads, D), torch.bfloat16, dev)
     status = _status(status, dev)
-    _launch("hpc_prompt_prologue", dev, _addr(qkv), n, _addr(cu_seqlens), batch, _addr(q_norm_w), _addr(k_norm_w),
-            float(eps), float(rope_theta), _addr(q_out), _addr(k_out), _addr(k_pages), _addr(v_pages), code, lay,
-            _addr(k_scale), _addr(v_scale), num_pages, P, _addr(block_table), block_table.shape[1], _addr(seq_lens),
-            num_heads, kv_heads, D, _addr(status))
+    _launch("hpc_prompt_prologue", dev, qkv.data_ptr(), n, cu_seqlens.data_ptr(), batch, q_norm_w.data_ptr(),
+            k_norm_w.data_ptr(), float(eps), float(rope_theta), q_out.data_ptr(), k_out.data_ptr(),
+            k_pages.data_ptr(), v_pages.data_ptr(), code, lay, _addr(k_scale), _addr(v_scale), num_pages, P,
+            block_table.data_ptr(), block_table.shape[1], _addr(seq_lens), num_heads, kv_heads, D, status.data_ptr())
     return q_out, k_out, status
 
 
@@ -848,9 +848,9 @@ def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_
     lse = _lse(lse, return_lse, n, Hq, dev)
     status = _status(status, dev)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    _launch("hpc_prompt_attention", dev, _addr(q), *qs, _addr(k), *ks, _addr(v), *vs, n, k.shape[0], _addr(cu_seqlens),
-            _addr(cu_seqlens_k), batch, Hq, k.shape[1], D, 1 if causal else 0, scale, _addr(out), _addr(lse),
-            _addr(status))
+    _launch("hpc_prompt_attention", dev, q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, n, k.shape[0],
+            cu_seqlens.data_ptr(), _addr(cu_seqlens_k), batch, Hq, k.shape[1], D, 1 if causal else 0, scale,
+            out.data_ptr(), _addr(lse), status.data_ptr())
     return out, lse, status
 
 
@@ -869,9 +869,9 @@ def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlen
     lse = _lse(lse, return_lse, n, Hq, dev)
     status = _status(status, dev)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    _launch("hpc_prompt_attention_paged", dev, _addr(q), *qs, _addr(k_pages), _addr(v_pages), code, lay, num_pages, P,
-            _addr(block_table), block_table.shape[1], _addr(seq_lens), n, _addr(cu_seqlens), batch, Hq, Hkv, D, scale,
-            _addr(out), _addr(lse), _addr(status))
+    _launch("hpc_prompt_attention_paged", dev, q.data_ptr(), *qs, k_pages.data_ptr(), v_pages.data_ptr(), code, lay,
+            num_pages, P, block_table.data_ptr(), block_table.shape[1], _addr(seq_lens), n, cu_seqlens.data_ptr(),
+            batch, Hq, Hkv, D, scale, out.data_ptr(), _addr(lse), status.data_ptr())
     return out, lse, status
 
 
@@ -925,9 +925,10 @@ def verify_drafts(draft_tokens, target_probs, draft_probs, uniforms, *, draft_le
     elif new_lens is not None:
         raise HpcError("new_lens needs seq_lens")
     status = _status(status, dev)
-    _launch("hpc_verify_drafts", dev, _addr(draft_tokens), _addr(target_probs), p_row, _addr(draft_probs), q_row,
-            HPC_FP32 if target_probs.dtype == torch.float32 else HPC_BF16, _addr(uniforms), _addr(draft_lens),
-            _addr(seq_lens), Bn, T, V, _addr(out_tokens), _addr(accepted), _addr(new_lens), _addr(status))
+    _launch("hpc_verify_drafts", dev, draft_tokens.data_ptr(), target_probs.data_ptr(), p_row, _addr(draft_probs),
+            q_row, HPC_FP32 if target_probs.dtype == torch.float32 else HPC_BF16, uniforms.data_ptr(),
+            _addr(draft_lens), _addr(seq_lens), Bn, T, V, out_tokens.data_ptr(), accepted.data_ptr(), _addr(new_lens),
+            status.data_ptr())
     return out_tokens, accepted, new_lens, status
 
 
@@ -978,9 +979,9 @@ def resize_pages(block_table, old_lens, new_lens, ref_count, page_size, *, block
     ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
     moves, n_moves = _moves(moves, n_moves, Bn, dev)
     status = _status(status, dev)
-    _launch("hpc_pages_resize", dev, _addr(block_table), _addr(table_out), Bn, M, int(page_size), _addr(old_lens),
-            _addr(new_lens), _addr(ref_count), _addr(ref_out), N, _addr(moves), moves.shape[0], _addr(n_moves),
-            _addr(status))
+    _launch("hpc_pages_resize", dev, block_table.data_ptr(), table_out.data_ptr(), Bn, M, int(page_size),
+            old_lens.data_ptr(), _addr(new_lens), ref_count.data_ptr(), ref_out.data_ptr(), N, moves.data_ptr(),
+            moves.shape[0], n_moves.data_ptr(), status.data_ptr())
     return PageUpdate(table_out, ref_out, moves, n_moves, status)
 
 
@@ -999,9 +1000,9 @@ def fork_pages(block_table, seq_lens, ref_count, parents, page_size, *, block_ta
     ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
     moves, n_moves = _moves(moves, n_moves, rows_out, dev)
     status = _status(status, dev)
-    _launch("hpc_pages_fork", dev, _addr(block_table), _addr(seq_lens), rows_in, _addr(parents), _addr(table_out),
-            _addr(lens_out), rows_out, M, int(page_size), _addr(ref_count), _addr(ref_out), N, _addr(moves),
-            moves.shape[0], _addr(n_moves), _addr(status))
+    _launch("hpc_pages_fork", dev, block_table.data_ptr(), _addr(seq_lens), rows_in, parents.data_ptr(),
+            table_out.data_ptr(), lens_out.data_ptr(), rows_out, M, int(page_size), ref_count.data_ptr(),
+            ref_out.data_ptr(), N, moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), status.data_ptr())
     return PageUpdate(table_out, ref_out, moves, n_moves, status, seq_lens=lens_out)
 
 
@@ -1014,8 +1015,9 @@ def compact_pages(block_table, ref_count, *, block_table_out=None, ref_count_out
     page_map = _buffer(page_map, "page_map", (N,), torch.int32, dev)
     moves, n_moves = _moves(moves, n_moves, N // 2, dev)
     status = _status(status, dev)
-    _launch("hpc_pages_compact", dev, _addr(block_table), _addr(table_out), Bn, M, _addr(ref_count), _addr(ref_out), N,
-            _addr(page_map), _addr(moves), moves.shape[0], _addr(n_moves), _addr(status))
+    _launch("hpc_pages_compact", dev, block_table.data_ptr(), table_out.data_ptr(), Bn, M, ref_count.data_ptr(),
+            ref_out.data_ptr(), N, page_map.data_ptr(), moves.data_ptr(), moves.shape[0], n_moves.data_ptr(),
+            status.data_ptr())
     return PageUpdate(table_out, ref_out, moves, n_moves, status, page_map=page_map)
 
 
@@ -1034,17 +1036,18 @@ def copy_pages(caches, moves, n_moves, *, status=None):
     status = _status(status, dev)
     if not caches:
         return status
+    shape, size = caches[0].shape, caches[0].element_size()
     for t in caches:
-        _need(t, "cache", device=dev)
-        if t.dim() < 2 or t.shape != caches[0].shape or t.element_size() != caches[0].element_size():
+        _want(t, "cache", t.dtype, dev)
+        if t.shape != shape or t.element_size() != size or len(shape) < 2:
             raise HpcError("the caches must be [num_pages, ...] tensors of one shape and element size")
-    num_pages = caches[0].shape[0]
+    num_pages = shape[0]
     if num_pages == 0:
         raise HpcError("the caches hold no pages")
-    page_bytes = caches[0][0].numel() * caches[0].element_size()
+    page_bytes = caches[0].numel() // num_pages * size
     ptrs = (ctypes.c_void_p * len(caches))(*[t.data_ptr() for t in caches])
-    _launch("hpc_pages_copy", dev, ptrs, len(caches), page_bytes, num_pages, _addr(moves), moves.shape[0],
-            _addr(n_moves), _addr(status))
+    _launch("hpc_pages_copy", dev, ptrs, len(caches), page_bytes, num_pages, moves.data_ptr(), moves.shape[0],
+            n_moves.data_ptr(), status.data_ptr())
     return status
 
 
