@@ -137,14 +137,28 @@ def _load(path=LIB):
     return lib
 
 
-_lib = _load()
+try:  # the short way in for calls in the common form; without it every call goes the long way
+    from . import _fastcall as _fast
+except ImportError:
+    _fast = None
+_FAST_CALLS = ("hpc_prompt_prologue", "hpc_prompt_attention", "hpc_prompt_attention_paged", "hpc_verify_drafts",
+               "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact", "hpc_pages_copy")
+
+
+def _bind(lib):
+    if _fast is not None:
+        _fast.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_CALLS))
+    return lib
+
+
+_lib = _bind(_load())
 
 
 def use_library(path: str = LIB):
     """Switch this module to another build of the library (e.g. the HPC_TRACE build, see
     ``build.build(trace=True)``); ``use_library()`` goes back to the default build."""
     global _lib, _path
-    _lib = _load(path)
+    _lib = _bind(_load(path))
     _path = path
 
 
@@ -787,6 +801,12 @@ def prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block
     [tokens, Hq + 2 Hkv, D], request r's tokens are rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 and the
     last of its seq_lens[r]. Returns (q_out [tokens, Hq, D], k_out [tokens, Hkv, D], status); rows of no
     request are left as they were."""
+    if _fast is not None:
+        r = _fast.prompt_prologue(qkv, cu_seqlens, q_norm_w, k_norm_w, k_pages, v_pages, block_table, seq_lens, num_heads,
+                                  kv_heads, _KV_DTYPES.get(kv_dtype), _LAYOUTS.get(kv_layout), k_scale, v_scale, eps,
+                                  rope_theta, q_out, k_out, status)
+        if r is not None:
+            return r
     _need(qkv, "qkv", torch.bfloat16)
     dev = qkv.device
     _want(q_norm_w, "q_norm_w", torch.float32, dev)
@@ -835,6 +855,10 @@ def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_
     bf16, possibly views into one qkv tensor; sequence r is rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 (of k and
     v: cu_seqlens_k, default the same), its queries the last of its keys. Returns (out bf16 [tokens, Hq, D],
     lse fp32 [tokens, Hq] or None, status); rows of no sequence are left as they were."""
+    if _fast is not None:
+        r = _fast.prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k, causal, sm_scale, out, lse, return_lse, status)
+        if r is not None:
+            return r
     qs = _strided(q, "q", None)
     dev = q.device
     ks, vs = _strided(k, "k", dev), _strided(v, "v", dev)
@@ -859,6 +883,11 @@ def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlen
     """Causal attention of packed prompts, or chunks of them, over the bf16 pages of the cache
     (``hpc_prompt_attention_paged``): the queries of request r are the last of its seq_lens[r] cached tokens.
     Returns (out bf16 [tokens, Hq, D], lse fp32 [tokens, Hq] or None, status)."""
+    if _fast is not None:
+        r = _fast.prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, _LAYOUTS.get(kv_layout),
+                                         sm_scale, out, lse, return_lse, status)
+        if r is not None:
+            return r
     qs = _strided(q, "q", None)
     dev = q.device
     n, Hq, D = q.shape
@@ -898,6 +927,11 @@ def verify_drafts(draft_tokens, target_probs, draft_probs, uniforms, *, draft_le
     [B, T], target_probs [B, T + 1, V] and draft_probs [B, T, V] (or None: one-hot drafts) in fp32 or bf16,
     uniforms fp32 [B, T + 1]. Rows may be padded (a view of a wider tensor). Returns (out_tokens [B, T + 1],
     accepted [B], new_lens [B] or None, status); new_lens needs seq_lens."""
+    if _fast is not None:
+        r = _fast.verify_drafts(draft_tokens, target_probs, draft_probs, uniforms, draft_lens, seq_lens, out_tokens,
+                                accepted, new_lens, status)
+        if r is not None:
+            return r
     _need(draft_tokens, "draft_tokens", torch.int32)
     dev = draft_tokens.device
     if draft_tokens.dim() != 2 or not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 3:
@@ -970,6 +1004,11 @@ def resize_pages(block_table, old_lens, new_lens, ref_count, page_size, *, block
     """Requests change from old_lens to new_lens tokens (``hpc_pages_resize``): pages are released, taken,
     and copied on write where a part-filled page is shared. Without output buffers the update is a new
     table and new counts; handing the inputs in as outputs updates them in place."""
+    if _fast is not None:
+        r = _fast.resize_pages(block_table, old_lens, new_lens, ref_count, page_size, block_table_out, ref_count_out,
+                               moves, n_moves, status)
+        if r is not None:
+            return PageUpdate(*r)
     dev, Bn, M, N = _pool(block_table, ref_count)
     for name, t in (("old_lens", old_lens), ("new_lens", new_lens)):
         _want(t, name, torch.int32, dev)
@@ -989,6 +1028,11 @@ def fork_pages(block_table, seq_lens, ref_count, parents, page_size, *, block_ta
                ref_count_out=None, moves=None, n_moves=None, status=None) -> PageUpdate:
     """New row r is old row parents[r], -1 for none (``hpc_pages_fork``): full pages are shared, a
     part-filled last page is copied for every child but the first, rows without children are released."""
+    if _fast is not None:
+        r = _fast.fork_pages(block_table, seq_lens, ref_count, parents, page_size, block_table_out, seq_lens_out,
+                             ref_count_out, moves, n_moves, status)
+        if r is not None:
+            return PageUpdate(*r)
     dev, rows_in, M, N = _pool(block_table, ref_count)
     _want(seq_lens, "seq_lens", torch.int32, dev)
     if seq_lens.numel() != rows_in:
@@ -1009,6 +1053,10 @@ def fork_pages(block_table, seq_lens, ref_count, parents, page_size, *, block_ta
 def compact_pages(block_table, ref_count, *, block_table_out=None, ref_count_out=None, page_map=None, moves=None,
                   n_moves=None, status=None) -> PageUpdate:
     """The pages in use move to the lowest ids (``hpc_pages_compact``); page_map names every page's new id."""
+    if _fast is not None:
+        r = _fast.compact_pages(block_table, ref_count, block_table_out, ref_count_out, page_map, moves, n_moves, status)
+        if r is not None:
+            return PageUpdate(*r)
     dev, Bn, M, N = _pool(block_table, ref_count)
     table_out = _buffer(block_table_out, "block_table_out", (Bn, M), torch.int32, dev)
     ref_out = _buffer(ref_count_out, "ref_count_out", (N,), torch.int32, dev)
@@ -1026,6 +1074,10 @@ def copy_pages(caches, moves, n_moves, *, status=None):
     [num_pages, ...] of one shape and element size, the K and V of every layer that shares the table.
     Returns status."""
     caches = list(caches)
+    if _fast is not None:
+        r = _fast.copy_pages(caches, moves, n_moves, status)
+        if r is not None:
+            return r
     _need(moves, "moves", torch.int32)
     dev = moves.device
     if moves.dim() != 2 or moves.shape[1] != 2:
