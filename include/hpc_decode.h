@@ -520,13 +520,24 @@ HPC_API int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_t* 
  * A query that sees no key (m_r < n_r) gets zeros and -inf. A sequence whose lengths do not hold together
  * (descending, or past tokens / kv_tokens) sets HPC_DEV_BAD_SEQLEN and is left out. Values of keys that a
  * query does not see never reach its result, infinities and NaN included. P is rounded to bf16 for its
- * product with V; sums and the softmax are fp32. */
+ * product with V; sums and the softmax are fp32.
+ *   work:    device uint32 [HPC_PROMPT_WORK_WORDS], zero at every call; left unspecified.
+ *   partial: device scratch of partial_bytes, 16-byte aligned, or NULL with 0: where the work of few queries on
+ *            many keys can be cut along the keys. hpc_prompt_attention_partial_bytes() is the most it uses;
+ *            with less, less is cut. Not used when no sequence can have more than HPC_PROMPT_SPLIT_KEYS keys
+ *            (kv_tokens, or max_pages_per_req * page_size).
+ * Calls that overlap on the GPU need work and partial of their own. A cut sequence's result depends on where it is
+ * cut (by the lengths of the batch) in the last bits, never on timing. */
+#define HPC_PROMPT_WORK_WORDS 8
+#define HPC_PROMPT_SPLIT_KEYS 1536
+HPC_API size_t hpc_prompt_attention_partial_bytes(int32_t head_dim); /* current device; 0 for a bad head_dim */
+
 HPC_API int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
                                  int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
                                  int64_t v_head_stride, int64_t tokens, int64_t kv_tokens, const int32_t* cu_seqlens,
                                  const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads, int32_t kv_heads,
                                  int32_t head_dim, int32_t causal, float sm_scale, void* out, float* lse,
-                                 uint32_t* status, void* stream);
+                                 uint32_t* work, void* partial, size_t partial_bytes, uint32_t* status, void* stream);
 
 /* hpc_prompt_attention, causal, with the keys and values of request r in the pages of the cache: its
  * seq_lens[r] cached tokens, the last cu_seqlens[r+1] - cu_seqlens[r] of which are the queries (a chunk of a
@@ -540,7 +551,8 @@ HPC_API int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride, in
                                        const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
                                        int64_t tokens, const int32_t* cu_seqlens, int32_t batch, int32_t num_heads,
                                        int32_t kv_heads, int32_t head_dim, float sm_scale, void* out, float* lse,
-                                       uint32_t* status, void* stream);
+                                       uint32_t* work, void* partial, size_t partial_bytes, uint32_t* status,
+                                       void* stream);
 
 /* ---- verification of drafted tokens -----------------------------------------------------
  * After hpc_decode_step_multi has run the target over the drafted tokens: which of them stand, and the

@@ -42,7 +42,8 @@ EXPORTS = ("hpc_step_record_bytes", "hpc_build_flags", "hpc_plan_workspace_bytes
            "hpc_decode_step_multi", "hpc_decode_step_multi_workspace_bytes", "hpc_decode_step_lse",
            "hpc_merge_lse", "hpc_wait_selftest", "hpc_merge_lse_gather", "hpc_gather_rows", "hpc_gather_pages",
            "hpc_prompt_prologue", "hpc_verify_drafts", "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact",
-           "hpc_pages_copy", "hpc_prompt_attention", "hpc_prompt_attention_paged")
+           "hpc_pages_copy", "hpc_prompt_attention", "hpc_prompt_attention_paged",
+           "hpc_prompt_attention_partial_bytes")
 
 
 class HpcError(RuntimeError):
@@ -124,9 +125,10 @@ def _load(path=LIB):
         "hpc_pages_compact": (ctypes.c_int, [vp, vp, i32, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp]),
         "hpc_pages_copy": (ctypes.c_int, [ctypes.POINTER(vp), i32, ctypes.c_int64, i32, vp, i32, vp, vp, vp]),
         "hpc_prompt_attention": (ctypes.c_int, [vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, vp, vp, i32, i32, i32,
-                                                i32, i32, fp, vp, vp, vp, vp]),
+                                                i32, i32, fp, vp, vp, vp, vp, sz, vp, vp]),
+        "hpc_prompt_attention_partial_bytes": (sz, [i32]),
         "hpc_prompt_attention_paged": (ctypes.c_int, [vp, i64, i64, vp, vp, ctypes.c_int, ctypes.c_int, i32, i32, vp, i32,
-                                                      vp, i64, vp, i32, i32, i32, i32, fp, vp, vp, vp, vp]),
+                                                      vp, i64, vp, i32, i32, i32, i32, fp, vp, vp, vp, vp, sz, vp, vp]),
         "hpc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "hpc_last_error": (ctypes.c_char_p, []),
         "hpc_abi_version": (ctypes.c_int, []),
@@ -142,7 +144,8 @@ try:  # the short way in for calls in the common form; without it every call goe
 except ImportError:
     _fast = None
 _FAST_CALLS = ("hpc_prompt_prologue", "hpc_prompt_attention", "hpc_prompt_attention_paged", "hpc_verify_drafts",
-               "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact", "hpc_pages_copy")
+               "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact", "hpc_pages_copy",
+               "hpc_prompt_attention_partial_bytes")
 
 
 def _bind(lib):
@@ -849,6 +852,19 @@ def _lse(lse, return_lse, n, heads, dev):
     return _buffer(lse, "lse", (n, heads), torch.float32, dev)
 
 
+PROMPT_WORK_WORDS, PROMPT_SPLIT_KEYS = 8, 1536
+
+
+def _prompt_scratch(max_keys, head_dim, dev):
+    """(work, partial, bytes) of one prompt attention call; partial only where sequences can be cut."""
+    work = torch.zeros(PROMPT_WORK_WORDS, dtype=torch.int32, device=dev)
+    if max_keys <= PROMPT_SPLIT_KEYS:
+        return work, None, 0
+    with torch.cuda.device(dev):
+        nbytes = _lib.hpc_prompt_attention_partial_bytes(head_dim)
+    return work, torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+
+
 def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_scale=None, out=None, lse=None,
                      return_lse=False, status=None):
     """Attention of packed prompts (``hpc_prompt_attention``): q [tokens, Hq, D], k / v [kv_tokens, Hkv, D] in
@@ -872,9 +888,10 @@ def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_
     lse = _lse(lse, return_lse, n, Hq, dev)
     status = _status(status, dev)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    work, partial, nbytes = _prompt_scratch(k.shape[0], D, dev)
     _launch("hpc_prompt_attention", dev, q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, n, k.shape[0],
             cu_seqlens.data_ptr(), _addr(cu_seqlens_k), batch, Hq, k.shape[1], D, 1 if causal else 0, scale,
-            out.data_ptr(), _addr(lse), status.data_ptr())
+            out.data_ptr(), _addr(lse), work.data_ptr(), _addr(partial), nbytes, status.data_ptr())
     return out, lse, status
 
 
@@ -898,9 +915,10 @@ def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlen
     lse = _lse(lse, return_lse, n, Hq, dev)
     status = _status(status, dev)
     scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    work, partial, nbytes = _prompt_scratch(block_table.shape[1] * P, D, dev)
     _launch("hpc_prompt_attention_paged", dev, q.data_ptr(), *qs, k_pages.data_ptr(), v_pages.data_ptr(), code, lay,
             num_pages, P, block_table.data_ptr(), block_table.shape[1], _addr(seq_lens), n, cu_seqlens.data_ptr(),
-            batch, Hq, Hkv, D, scale, out.data_ptr(), _addr(lse), status.data_ptr())
+            batch, Hq, Hkv, D, scale, out.data_ptr(), _addr(lse), work.data_ptr(), _addr(partial), nbytes, status.data_ptr())
     return out, lse, status
 
 

@@ -36,6 +36,7 @@ struct Api {
   decltype(&hpc_pages_fork) pages_fork;
   decltype(&hpc_pages_compact) pages_compact;
   decltype(&hpc_pages_copy) pages_copy;
+  decltype(&hpc_prompt_attention_partial_bytes) partial_bytes;
 } api = {};
 
 // Thrown for whatever is not the common form.
@@ -112,19 +113,25 @@ struct Call {
     }
     return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, dev), std::nullopt);
   }
-  // The caller's status word, or a zeroed one: words are zeroed 128 at a time on the stream that uses them.
+  // The caller's status word, or a zeroed one.
   Tensor status(PyObject* o) const {
     if (given(o)) {
       const Tensor& t = tensor(o);
       in(t, at::kInt);
       return t;
     }
+    return zeroed<1, 128>();
+  }
+  // kWords zeroed words that nothing else has had: kTimes of them are zeroed at a time on the stream that uses
+  // them, since a memset of its own for each call costs as much as a small kernel.
+  template <int64_t kWords, int64_t kTimes>
+  Tensor zeroed() const {
     require(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None);
-    static auto* words = new std::unordered_map<void*, std::vector<Tensor>>[64];  // never freed: the driver may be gone
+    static auto* pieces = new std::unordered_map<void*, std::vector<Tensor>>[64];  // never freed: the driver may be gone
     require(dev < 64);
-    std::vector<Tensor>& left = words[dev][stream];
+    std::vector<Tensor>& left = pieces[dev][stream];
     if (left.empty())
-      left = at::zeros({128}, at::TensorOptions().dtype(at::kInt).device(c10::Device(c10::kCUDA, dev))).split(1);
+      left = at::zeros({kWords * kTimes}, at::TensorOptions().dtype(at::kInt).device(c10::Device(c10::kCUDA, dev))).split(kWords);
     Tensor t = std::move(left.back());
     left.pop_back();
     return t;
@@ -369,6 +376,18 @@ float scale_of(PyObject* o, int64_t D) {
   return static_cast<float>(given(o) ? number(o) : 1.0 / std::sqrt(static_cast<double>(D)));
 }
 
+// Zeroed work words and, where sequences can be cut, the scratch for their parts. Both go back to the allocator
+// when the call returns; it hands them out again behind this call on the stream.
+struct Scratch {
+  Tensor work, partial;
+  Scratch(const Call& c, int64_t max_keys, int64_t head_dim) : work(c.zeroed<HPC_PROMPT_WORK_WORDS, 128>()) {
+    if (max_keys > HPC_PROMPT_SPLIT_KEYS && (head_dim == 64 || head_dim == 128))
+      partial = c.out(Py_None, at::kByte, {static_cast<int64_t>(api.partial_bytes(static_cast<int32_t>(head_dim)))});
+  }
+  void* at() const { return partial.defined() ? partial.data_ptr() : nullptr; }
+  size_t bytes() const { return partial.defined() ? partial.numel() : 0; }
+};
+
 Tensor lse_out(const Call& c, PyObject* o, PyObject* wanted, const Rows& q) {
   if (!given(o) && wanted != Py_True) return Tensor();
   return c.out(o, at::kFloat, {q.tokens, q.heads});
@@ -387,11 +406,13 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* cu_k = static_cast<const int32_t*>(c.optional(a[4], at::kInt, cu.numel()));
     const Tensor out = c.out(a[7], at::kBFloat16, {q.tokens, q.heads, q.D}), lse = lse_out(c, a[8], a[9], q),
                  status = c.status(a[10]);
+    const Scratch scratch(c, k.tokens, q.D);
     done(api.prompt_attention(q.at, q.token_stride, q.head_stride, k.at, k.token_stride, k.head_stride, v.at,
                               v.token_stride, v.head_stride, q.tokens, k.tokens,
                               static_cast<const int32_t*>(c.in(cu, at::kInt)), cu_k, int32(cu.numel() - 1), int32(q.heads),
                               int32(k.heads), int32(q.D), a[5] == Py_True, scale_of(a[6], q.D), out.data_ptr(),
-                              lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(status), c.stream));
+                              lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
+                              scratch.bytes(), word(status), c.stream));
     return tuple(out, lse, status);
   });
 }
@@ -407,11 +428,13 @@ PyObject* prompt_attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     require(PyBool_Check(a[10]));
     const Tensor out = c.out(a[8], at::kBFloat16, {q.tokens, q.heads, q.D}), lse = lse_out(c, a[9], a[10], q),
                  status = c.status(a[11]);
+    const Scratch scratch(c, static_cast<int64_t>(r.max_pages) * cache.page_size, q.D);
     done(api.prompt_attention_paged(q.at, q.token_stride, q.head_stride, cache.k, cache.v, HPC_BF16,
                                     nhd ? HPC_NHD : HPC_HND, cache.num_pages, cache.page_size, r.table, r.max_pages,
                                     r.lens, q.tokens, r.cu, r.batch, int32(q.heads), cache.kv_heads, int32(q.D),
                                     scale_of(a[7], q.D), out.data_ptr(),
-                                    lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(status),
+                                    lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
+                              scratch.bytes(), word(status),
                                     c.stream));
     return tuple(out, lse, status);
   });
@@ -419,12 +442,12 @@ PyObject* prompt_attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // bind(addresses): the library's functions, in the order of Api.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* f[8];
-  if (n != 8) {
-    PyErr_SetString(PyExc_ValueError, "bind takes eight addresses");
+  void* f[9];
+  if (n != 9) {
+    PyErr_SetString(PyExc_ValueError, "bind takes nine addresses");
     return nullptr;
   }
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 9; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -434,7 +457,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   api = {reinterpret_cast<decltype(api.prompt_prologue)>(f[0]), reinterpret_cast<decltype(api.prompt_attention)>(f[1]),
          reinterpret_cast<decltype(api.prompt_attention_paged)>(f[2]), reinterpret_cast<decltype(api.verify_drafts)>(f[3]),
          reinterpret_cast<decltype(api.pages_resize)>(f[4]), reinterpret_cast<decltype(api.pages_fork)>(f[5]),
-         reinterpret_cast<decltype(api.pages_compact)>(f[6]), reinterpret_cast<decltype(api.pages_copy)>(f[7])};
+         reinterpret_cast<decltype(api.pages_compact)>(f[6]), reinterpret_cast<decltype(api.pages_copy)>(f[7]),
+         reinterpret_cast<decltype(api.partial_bytes)>(f[8])};
   Py_RETURN_NONE;
 }
 

@@ -21,10 +21,14 @@
 // product (relative error 2^-9 per weight, which the output's own bf16 rounding matches); the sum l_i is
 // taken over the unrounded values.
 //
-// Persistent CTAs (one per SM) take units longest first: units are put in 64 buckets by the number of
-// keys they reach and dealt in a snake over the CTAs, from a table that every CTA builds from cu_seqlens
-// at the start. The producer warp looks the units up, ahead of the others, and loads Q and
-// a ring of K and V blocks by TMA (swizzled planes of 64 elements).
+// Persistent CTAs (one per SM) take units longest first from a counter: units are put in 64 buckets by the number
+// of keys they reach, in a table that every CTA builds from cu_seqlens at the start. Where a bucket's units are
+// longer than a CTA's share of all blocks (few heads, or a few new tokens on a long cache), they are cut into
+// parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second kernel, launched behind
+// this one, joins them (a last part that joined the others by itself took 40 us for 18 parts of a tile: one SM
+// reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 294 us uncut, @@SPLIT@@ us so.
+// The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
+// (swizzled planes of 64 elements).
 //
 // Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 issues the products with
 // K, warp 10 those with V, warp 9 looks up units and loads, warp 11 checks V. A softmax thread holds the 128
@@ -49,6 +53,9 @@ constexpr uint32_t kPaCols = 512;       // S 0, P_A 128, P_B 192, O_A 256, O_B 3
 constexpr float kPaMove = 8.f;
 constexpr int kPaSplit = 2;               // P is handed over in two parts: after 64 keys, and whole
 constexpr int kPaStages64 = 8, kPaStages128 = 5;
+constexpr int kPaMinPart = 6;           // blocks: a shorter part costs more in the joining than it saves
+constexpr int kPaMaxParts = 32;
+constexpr int kPaCuts = 512;            // cut units that the scratch can describe, ahead of the slots
 
 template <int D>
 struct PaLayout {
@@ -59,17 +66,27 @@ struct PaLayout {
   static constexpr int kBytes = kOffRing + kStages * kTile + 1024;  // + alignment slack
 };
 
-// One unit of work, as the producer publishes it.
+// One unit of work, or a part of it, as the producer publishes it.
 struct PaUnit {
   int32_t valid;
   int32_t q0, q_end;  // row of q of the first token; end of the sequence
   int32_t kv0;        // packed: row of key 0; paged: the request
   int32_t keys;       // keys of the sequence
   int32_t vis;        // keys that the unit's first token sees, one more for each token after it
-  int32_t blocks[2];  // key blocks of tile A and B
+  int32_t blocks[2];  // key blocks of tile A and B in this part
   int32_t kvh;
-  int32_t pad[3];
+  int32_t from;       // first block of the part
+  int32_t part;       // which part
+  int32_t parts[2];   // parts that hold blocks of tile A and B
+  int32_t slot;       // the part's place in the scratch; those of one unit are Hkv apart
+  int32_t pad[2];
 };
+
+// A cut unit, as the joining kernel finds it at the head of the scratch.
+struct PaCut {
+  int32_t q0, q_end, kvh, slot, parts[2], pad[2];
+};
+constexpr size_t kPaCutBytes = kPaCuts * sizeof(PaCut);
 
 struct PaArgs {
   const int32_t* cu_q;
@@ -81,9 +98,12 @@ struct PaArgs {
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
+  uint32_t* work;  // units taken, units cut; zero at the start
+  PaCut* cuts;
+  float* partial;  // [slots][2 tiles][m 128, l 128, O (D / 4) x 128 x 4]
   int64_t tokens, kv_tokens, max_pages;
   float scale_log2, scale;
-  int32_t batch, Hq, Hkv, group, causal, P, num_pages, nhd;
+  int32_t batch, Hq, Hkv, group, causal, P, num_pages, nhd, slots;
 };
 
 struct PaBars {
@@ -99,11 +119,13 @@ struct PaShared {
   PaBars bars;
   PaUnit unit[kPaTileRing];
   int32_t found[kPaTileRing];  // the unit's partly visible blocks hold a value that is not finite
-  int32_t base[kPaBuckets];   // units' token tiles in the buckets above
-  int32_t count[kPaBuckets];
+  int32_t base[kPaBuckets];   // parts of token tiles in the buckets above
+  int32_t count[kPaBuckets];  // and in this one
+  int32_t parts[kPaBuckets];  // per tile of the bucket
+  unsigned long long blocks;  // of all token tiles, about
   int32_t hist[kPaBuckets + 1], rem[kPaBuckets + 1];
   int32_t span;               // extent of the cost axis
-  int32_t tiles;              // all token tiles
+  int32_t tiles;              // parts of all token tiles
   int32_t bad;
   uint32_t tmem;
 };
@@ -149,9 +171,11 @@ __device__ __forceinline__ void swap_pieces(uint4& a, uint4& b, bool upper, int 
 
 // One row by one warp from global memory, without a product over keys that it does not see. For units whose
 // partly visible blocks of V hold infinities or NaN: there the tensor cores' 0 * v would reach rows that do not
-// see v. Such a prompt is broken; this keeps it from changing the tokens before the break.
+// see v. Such a prompt is broken; this keeps it from changing the tokens before the break. Keys [from, vis);
+// to the output, or as part of a unit to row `r` of its slot.
 template <int D, bool kPaged>
-__device__ __noinline__ void pa_row(const PaArgs& a, const PaUnit& x, int32_t token, int32_t head_in, int32_t vis) {
+__device__ __noinline__ void pa_row(const PaArgs& a, const PaUnit& x, int32_t token, int32_t head_in, int32_t from,
+                                    int32_t vis, float* slot, int32_t r) {
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31;
   const int32_t head = x.kvh * a.group + head_in;
@@ -160,7 +184,7 @@ __device__ __noinline__ void pa_row(const PaArgs& a, const PaUnit& x, int32_t to
 #pragma unroll
   for (int e = 0; e < kPer; ++e) qf[e] = __bfloat162float(q[lane + 32 * e]);
   float m = -INFINITY, l = 0.f;
-  for (int32_t j = 0; j < vis; ++j) {
+  for (int32_t j = from; j < vis; ++j) {
     const __nv_bfloat16 *k, *v;
     if (kPaged) {
       int32_t page = a.table[static_cast<int64_t>(x.kv0) * a.max_pages + j / a.P];
@@ -190,6 +214,18 @@ __device__ __noinline__ void pa_row(const PaArgs& a, const PaUnit& x, int32_t to
     l += p;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) o[e] = fmaf(p, __bfloat162float(v[lane + 32 * e]), o[e]);
+  }
+  if (slot) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int d = lane + 32 * e;
+      slot[2 * kPaRows + ((d >> 2) * kPaRows + r) * 4 + (d & 3)] = o[e];
+    }
+    if (lane == 0) {
+      slot[r] = m;
+      slot[kPaRows + r] = l;
+    }
+    return;
   }
   const bool some = l > 0.f || l != l;
   const int64_t at = static_cast<int64_t>(token) * a.Hq + head;
@@ -232,6 +268,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
     fence_barrier_init();
     sh.span = 0;
+    sh.blocks = 0;
     sh.bad = 0;
   }
   for (int i = threadIdx.x; i <= kPaBuckets; i += kPaThreads) sh.hist[i] = sh.rem[i] = 0;
@@ -251,13 +288,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   // ---- the table of units: 64 buckets of the cost axis
   {
     int32_t span = 0, bad = 0;
+    int64_t rows = 0;  // keys that the tiles reach
     for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
       int32_t q0, q1, k0, keys, lo, hi;
       bad |= !pa_sequence(a, kPaged, s, q0, q1, k0, keys);
       pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
       if (hi > span) span = hi;
+      rows += (static_cast<int64_t>(hi) * (hi + 1) - static_cast<int64_t>(lo) * (lo + 1)) / 2 * tokens_per_unit;
     }
     atomicMax(&sh.span, span);
+    if (rows > 0) atomicAdd(&sh.blocks, static_cast<unsigned long long>(rows / kPaKeys + 1));
     if (bad) sh.bad = 1;
     __syncthreads();
     if (threadIdx.x == 0 && sh.bad && blockIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
@@ -289,11 +329,30 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int32_t h0 = sh.hist[b0], h1 = sh.hist[b1];
     const int32_t above = sh.hist[kPaBuckets] + scan(h0 + h1) - h0 - h1;  // sequences that end past bucket b0
     const int32_t c0 = above * width + sh.rem[b0], c1 = (above + h0) * width + sh.rem[b1];
-    const int32_t upto = scan(c0 + c1);
-    sh.count[b0] = c0;
-    sh.count[b1] = c1;
-    sh.base[b0] = upto - c0 - c1;
-    sh.base[b1] = upto - c1;
+    // Parts per tile: about a CTA's share of all blocks each, as long as the scratch has a place for them. The
+    // buckets that are cut come first, so that a part's number is its place.
+    const int64_t all = static_cast<int64_t>(sh.blocks) * a.Hkv, share = (all + gridDim.x - 1) / gridDim.x;
+    const int64_t length = share > kPaMinPart ? share : kPaMinPart;
+    auto cut = [&](int b) -> int32_t {
+      const int64_t most = ((b + 1ll) * width + 1) * tokens_per_unit / kPaKeys + 1, least = static_cast<int64_t>(b) * width * tokens_per_unit / kPaKeys;
+      if (a.slots == 0 || most <= length || 2 * least < length) return 1;
+      const int64_t n = (most + length - 1) / length;
+      return static_cast<int32_t>(n < kPaMaxParts ? n : kPaMaxParts);
+    };
+    int32_t p0 = cut(b0), p1 = cut(b1);
+    const int64_t room = a.slots / a.Hkv;
+    {
+      const int32_t end = scan(c0 * p0 + c1 * p1);
+      if (end - c1 * p1 > room) p0 = 1;
+      if (end > room) p1 = 1;
+    }
+    const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
+    sh.parts[b0] = p0;
+    sh.parts[b1] = p1;
+    sh.count[b0] = n0;
+    sh.count[b1] = n1;
+    sh.base[b0] = upto - n0 - n1;
+    sh.base[b1] = upto - n1;
     if (lane == 31) sh.tiles = upto;
   }
   __syncthreads();
@@ -335,7 +394,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       int32_t vis_min = a.causal ? x.vis + t * tokens_per_tile : x.keys;
       if (vis_min > x.keys) vis_min = x.keys;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nb && ok; ++j) {
+      for (int j = x.from; j < x.from + nb && ok; ++j) {
         wait(sh.bars.s_full[t], done & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -393,11 +452,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
         const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-        if ((j + 1) * kPaKeys > x.keys && (t == 0 || j >= x.blocks[0])) {
+        if ((j + 1) * kPaKeys > x.keys && (t == 0 || j >= x.from + x.blocks[0])) {
           // Rows of V past the last key hold another sequence's values or what the memory held: zero, so that
           // 0 * v stays 0. The fill is the only one that its parity can mean: the stage's fill before was read
           // by products that this block's S follows.
-          const uint32_t f = fill + 2 * j + 1;
+          const uint32_t f = fill + 2 * (j - x.from) + 1;
           wait(sh.bars.kv_full[f % L::kStages], (f / L::kStages) & 1);
           ok = __all_sync(0xffffffffu, ok);
           uint8_t* vt = ring + (f % L::kStages) * L::kTile;
@@ -445,27 +504,55 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const bool found = sh.found[slot] != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh.bars.unit_free[slot]));
+      const int parts = t == 0 ? x.parts[0] : x.parts[1];
+      if (nb == 0 && (x.part > 0 || parts > 0)) {  // another part has this tile's keys
+        tc_fence_before();
+        continue;
+      }
+      const bool live = x.q0 + tok < x.q_end;
+      float* slot_at = parts > 1 ? a.partial + (static_cast<int64_t>(x.slot) * 2 + t) * (kPaRows * (D + 2)) : nullptr;
       if (found) {
         // 0 * v is not 0 for some v that a row does not see: the rows of this tile one by one
         for (int i = 0; i < 32; ++i) {
           const int32_t rk = (row & ~31) + i, tk = t * tokens_per_tile + (rk >> group_shift);
-          if (x.q0 + tk < x.q_end) pa_row<D, kPaged>(a, x, x.q0 + tk, rk & (a.group - 1), min(x.vis + tk, x.keys));
+          const int32_t seen = min(min(x.vis + tk, x.keys), parts > 1 ? (x.from + nb) * kPaKeys : x.keys);
+          if (x.q0 + tk < x.q_end) pa_row<D, kPaged>(a, x, x.q0 + tk, rk & (a.group - 1), x.from * kPaKeys, seen, slot_at, rk);
+        }
+        if (parts <= 1) {
+          tc_fence_before();
+          continue;
+        }
+      }
+      if (parts > 1) {
+        // ---- a part: its state to the scratch, row by row of the tile side by side
+        if (!found) {
+          if (live) {
+            slot_at[row] = m;
+            slot_at[kPaRows + row] = l;
+          }
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            umma::ld32(o_at + c0, o);
+            float4* at = reinterpret_cast<float4*>(slot_at + 2 * kPaRows) + (c0 / 4) * kPaRows + row;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (live) at[i * kPaRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
         }
         tc_fence_before();
         continue;
       }
-      const bool some = l > 0.f || l != l;  // a NaN stays one; a row without keys is zero
-      const float inv = some ? 1.f / l : 0.f;
-      if (a.lse && x.q0 + tok < x.q_end)
-        a.lse[static_cast<int64_t>(x.q0 + tok) * a.Hq + x.kvh * a.group + row % a.group] = some ? m * a.scale + logf(l) : -INFINITY;
+      // ---- the whole unit; a NaN stays one; a row without keys is zero (O then holds anything).
       // A thread holds a row of O. Four lanes exchange 16-byte pieces of their rows, so that each stores 64
       // bytes of a row with its neighbours: whole sectors (16 bytes of every row at a time took 3800 cycles).
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       __nv_bfloat16* dst[4];
-      bool live[4];
+      bool there[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int32_t rk = (row & ~3) + k, tk = x.q0 + t * tokens_per_tile + (rk >> group_shift);
-        live[k] = tk < x.q_end;
+        there[k] = tk < x.q_end;
         dst[k] = a.out + (static_cast<int64_t>(tk) * a.Hq + x.kvh * a.group + (rk & (a.group - 1))) * D + 8 * (lane & 3);
       }
 #pragma unroll
@@ -474,7 +561,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         umma::ld32(o_at + c0, o);
         uint4 w[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = nb > 0 ? o[i] * inv : 0.f;  // without keys O holds anything
+        for (int i = 0; i < 32; ++i) o[i] = nb > 0 ? o[i] * inv : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]), pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
@@ -485,8 +572,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         swap_pieces(w[1], w[3], lane & 2, 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (live[k]) *reinterpret_cast<uint4*>(dst[k] + c0) = w[k];
+          if (there[k]) *reinterpret_cast<uint4*>(dst[k] + c0) = w[k];
       }
+      if (a.lse && live)
+        a.lse[static_cast<int64_t>(x.q0 + tok) * a.Hq + x.kvh * a.group + row % a.group] =
+            l > 0.f || l != l ? m * a.scale + logf(l) : -INFINITY;
       tc_fence_before();
     }
     if (err && lane == 0) atomicOr(a.status, err);
@@ -496,9 +586,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // ------------------------------------------------------------------ units and loads
       uint32_t fill = 0;  // ring fills so far
       int32_t n_unit = 0, n_q = 0;
-      for (int64_t k = 0;; ++k) {
-        // the k-th unit of this CTA, in a snake over the CTAs
-        const int64_t u = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      for (bool begun = false;; begun = true) {
+        int64_t u = blockIdx.x;
+        if (begun) {
+          if (lane == 0) u = static_cast<int64_t>(gridDim.x) + atomicAdd(a.work, 1u);
+          u = __shfl_sync(0xffffffffu, u, 0);
+        }
         PaUnit x = {};
         x.valid = u < units;
         if (x.valid) {
@@ -508,7 +601,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           uint32_t m0 = __ballot_sync(0xffffffffu, tile >= sh.base[lane] && tile < sh.base[lane] + sh.count[lane]);
           uint32_t m1 = __ballot_sync(0xffffffffu, tile >= sh.base[lane + 32] && tile < sh.base[lane + 32] + sh.count[lane + 32]);
           const int b = m0 ? __ffs(m0) - 1 : 32 + __ffs(m1) - 1;
-          int32_t rank = tile - sh.base[b];
+          const int32_t parts = sh.parts[b];
+          int32_t rank = (tile - sh.base[b]) / parts;
+          x.part = tile - sh.base[b] - rank * parts;
+          x.slot = parts > 1 ? static_cast<int32_t>(u) : 0;
           // sequence: prefix of the tiles that each has in the bucket
           for (int32_t s0 = 0; s0 < a.batch; s0 += 32) {
             const int32_t s = s0 + lane;
@@ -546,16 +642,31 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 if (seen > keys) seen = keys;
                 x.blocks[t] = first < q1 && seen > 0 ? (seen + kPaKeys - 1) / kPaKeys : 0;
               }
+              // the part's blocks
+              int32_t length = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
+              if (parts > 1) {
+                length = (length + parts - 1) / parts;
+                if (length < kPaMinPart) length = kPaMinPart;
+              }
+              x.from = x.part * length;
+              for (int t = 0; t < 2; ++t) {
+                const int32_t have = x.blocks[t], left = have - x.from;
+                x.parts[t] = length > 0 ? (have + length - 1) / length : 0;
+                x.blocks[t] = left < 0 ? 0 : (left < length ? left : length);
+              }
               break;
             }
             rank -= __shfl_sync(0xffffffffu, inc, 31);
           }
         }
+        if (x.valid && x.part > 0 && x.blocks[0] == 0 && x.blocks[1] == 0) continue;  // fewer parts than the bucket's
         const int slot = n_unit % kPaTileRing;
         if (n_unit >= kPaTileRing) wait(sh.bars.unit_free[slot], ((n_unit / kPaTileRing) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) x.valid = 0;
         if (lane == 0) {
+          if (x.valid && x.part == 0 && (x.parts[0] > 1 || x.parts[1] > 1))
+            a.cuts[atomicAdd(a.work + 1, 1u)] = {x.q0, x.q_end, x.kvh, x.slot, {x.parts[0], x.parts[1]}, {}};
           sh.unit[slot] = x;
           mbar_arrive(bar(sh.bars.unit_full[slot]));
         }
@@ -584,14 +695,14 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               mbar_arrive_expect_tx(bar(sh.bars.kv_full[st]), L::kTile);
               for (int pl = 0; pl < L::kPlanes; ++pl)
                 tma_load_4d(smem_u32(ring) + st * L::kTile + pl * kPaPlane, (f & 1) ? &tm_v : &tm_k,
-                            bar(sh.bars.kv_full[st]), 64 * pl, x.kvh, x.kv0 + (f >> 1) * kPaKeys, 0);
+                            bar(sh.bars.kv_full[st]), 64 * pl, x.kvh, x.kv0 + (x.from + (f >> 1)) * kPaKeys, 0);
             }
           }
         } else {
           // 32 page ids at a time; pages of one block never straddle two batches of ids
-          const int32_t* row = a.table + static_cast<int64_t>(x.kv0) * a.max_pages;
           const int per_block = kPaKeys / a.P;
-          const int32_t live = (x.keys + a.P - 1) / a.P;  // pages that hold keys
+          const int32_t* row = a.table + static_cast<int64_t>(x.kv0) * a.max_pages + x.from * per_block;
+          const int32_t live = (x.keys + a.P - 1) / a.P - x.from * per_block;  // pages that hold keys, from the part on
           for (int32_t p0 = 0; p0 < nb * per_block && ok; p0 += 32) {
             int32_t id = 0;
             if (p0 + lane < live && p0 + lane < nb * per_block) {
@@ -644,6 +755,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int32_t valid = sh.unit[slot].valid, keys = sh.unit[slot].keys;
+        const int32_t from = sh.unit[slot].from;
         const int32_t whole = a.causal ? sh.unit[slot].vis : keys;  // keys that every row of the unit sees
         const int nb = max(sh.unit[slot].blocks[0], sh.unit[slot].blocks[1]);
         if (!valid) break;
@@ -651,7 +763,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         for (int f = 0; f < 2 * nb && ok; ++f) {
           wait(sh.bars.kv_full[stage], phase);
           ok = __all_sync(0xffffffffu, ok);
-          const int32_t first = (f >> 1) * kPaKeys;
+          const int32_t first = (from + (f >> 1)) * kPaKeys;
           if (ok && (f & 1) && whole < keys && first + kPaKeys > whole) {
             const int32_t rows = keys - first < kPaKeys ? keys - first : kPaKeys;  // those past it are zeroed
             // 0 * v added up is 0 for finite v, and a NaN from the first one that is not
@@ -782,6 +894,61 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   }
 }
 
+// Joins the parts of cut units by log-sum-exp: M = max m_i, w_i = 2^(c (m_i - M)), out = sum w_i O_i / sum w_i l_i.
+// A block takes four columns of a tile, a thread per row, so that the parts are read side by side and the whole
+// GPU reads them. Parts are added in order: the same result every time.
+constexpr int kPaJoin = 8;  // parts loaded together
+template <int D>
+__global__ void __launch_bounds__(kPaRows) prompt_join_kernel(const PaArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t cuts = a.work[1];
+  const int row = threadIdx.x, tokens_per_tile = kPaRows / a.group;
+  constexpr int64_t kTileFloats = kPaRows * (D + 2);
+  for (uint32_t u = blockIdx.x; u < cuts * (2 * (D / 4)); u += gridDim.x) {
+    const int c4 = u % (D / 4), t = u / (D / 4) % 2;
+    const PaCut x = a.cuts[u / (2 * (D / 4))];
+    const int parts = x.parts[t], token = x.q0 + t * tokens_per_tile + row / a.group;
+    if (parts <= 1 || token >= x.q_end) continue;
+    const float* first = a.partial + (static_cast<int64_t>(x.slot) * 2 + t) * kTileFloats;
+    const int64_t apart = static_cast<int64_t>(a.Hkv) * 2 * kTileFloats;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += kPaJoin) {
+      float mi[kPaJoin], li[kPaJoin];
+      float4 v[kPaJoin];
+#pragma unroll
+      for (int i = 0; i < kPaJoin; ++i) {
+        const bool have = i0 + i < parts;
+        const float* at = first + (have ? i0 + i : i0) * apart;
+        mi[i] = have ? at[row] : -INFINITY;
+        li[i] = have ? at[kPaRows + row] : 0.f;
+        v[i] = reinterpret_cast<const float4*>(at + 2 * kPaRows)[c4 * kPaRows + row];
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kPaJoin; ++i) top = fmaxf(top, mi[i]);
+      const float shrink = m == -INFINITY ? 0.f : ex2((m - top) * a.scale_log2);
+      m = top;
+      l = l == 0.f ? 0.f : l * shrink;
+      o = make_float4(o.x * shrink, o.y * shrink, o.z * shrink, o.w * shrink);
+#pragma unroll
+      for (int i = 0; i < kPaJoin; ++i) {
+        // a part without keys has no weight (its O may be anything), but a NaN of its sum stays
+        const float w = mi[i] == -INFINITY ? 0.f : ex2((mi[i] - m) * a.scale_log2);
+        l += li[i] != li[i] ? li[i] : li[i] * w;
+        if (w != 0.f) o = make_float4(fmaf(w, v[i].x, o.x), fmaf(w, v[i].y, o.y), fmaf(w, v[i].z, o.z), fmaf(w, v[i].w, o.w));
+      }
+    }
+    const bool some = l > 0.f || l != l;
+    const float inv = some ? 1.f / l : 0.f;
+    const int64_t at = static_cast<int64_t>(token) * a.Hq + x.kvh * a.group + row % a.group;
+    *reinterpret_cast<uint2*>(a.out + at * D + 4 * c4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && c4 == 0) a.lse[at] = some ? m * a.scale + logf(l) : -INFINITY;
+  }
+}
+
 // ---------------------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------------------
@@ -838,18 +1005,32 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
   // units: at most one part-filled per sequence and kv head
   const int64_t per_unit = 2 * kPaRows / a.group;
   const int64_t most = (a.tokens / per_unit + (a.batch < a.tokens ? a.batch : a.tokens)) * a.Hkv;
-  const int grid = static_cast<int>(most < sms ? most : sms);
+  const int grid = a.slots > 0 ? sms : static_cast<int>(most < sms ? most : sms);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kPaThreads), static_cast<size_t>(L::kBytes), stream, q, k, v, a);
   if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_attention_kernel: %s", cudaGetErrorString(e));
-  return check_launch("prompt_attention_kernel");
+  const int rc = check_launch("prompt_attention_kernel");
+  if (rc != HPC_OK || a.slots == 0) return rc;
+  const cudaError_t j = launch_pdl(prompt_join_kernel<D>, dim3(4 * sms), dim3(kPaRows), 0, stream, a);
+  if (j != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_join_kernel: %s", cudaGetErrorString(j));
+  return check_launch("prompt_join_kernel");
+}
+
+size_t pa_slot_bytes(int32_t head_dim) { return static_cast<size_t>(2) * kPaRows * (head_dim + 2) * sizeof(float); }
+
+// Two parts for every SM: units are cut into a share of the blocks each.
+size_t pa_most_slots() {
+  const size_t n = 2 * static_cast<size_t>(device_sm_count() > 0 ? device_sm_count() : 148);
+  return n < kPaCuts ? n : kPaCuts;
 }
 
 // What both entry points check of the queries and the shape; fills the common arguments and q's map.
 int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t tokens, const int32_t* cu_seqlens,
               int32_t batch, int32_t num_heads, int32_t kv_heads, int32_t head_dim, float sm_scale, void* out,
-              float* lse, uint32_t* status, PaArgs& a, CUtensorMap* map) {
+              float* lse, uint32_t* work, void* partial, size_t partial_bytes, int64_t max_keys, uint32_t* status,
+              PaArgs& a, CUtensorMap* map) {
   if (tokens < 0 || tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "tokens out of range");
-  if (!cu_seqlens || !status || (tokens > 0 && (!q || !out))) return fail(HPC_ERR_ARG, "null pointer argument");
+  if (!cu_seqlens || !status || !work || (tokens > 0 && (!q || !out)) || (partial_bytes > 0 && !partial))
+    return fail(HPC_ERR_ARG, "null pointer argument");
   if (batch < 1 || num_heads < 1 || kv_heads < 1) return fail(HPC_ERR_ARG, "sizes must be >= 1");
   if (num_heads % kv_heads) return fail(HPC_ERR_SHAPE, "num_heads %% kv_heads != 0");
   const int32_t g = num_heads / kv_heads;
@@ -860,6 +1041,15 @@ int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int6
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.status = status;
+  a.work = work;
+  if (!aligned16(partial)) return fail(HPC_ERR_ALIGN, "partial must be 16-byte aligned");
+  // units are cut only where some sequence can be long enough
+  if (max_keys > HPC_PROMPT_SPLIT_KEYS && partial_bytes > kPaCutBytes) {
+    const size_t room = (partial_bytes - kPaCutBytes) / pa_slot_bytes(head_dim);
+    a.slots = static_cast<int32_t>(room < pa_most_slots() ? room : pa_most_slots());
+    a.cuts = static_cast<PaCut*>(partial);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(partial) + kPaCutBytes);
+  }
   a.tokens = tokens;
   a.scale = sm_scale;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
@@ -882,16 +1072,21 @@ int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int6
 
 using namespace hpc;
 
+extern "C" size_t hpc_prompt_attention_partial_bytes(int32_t head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return kPaCutBytes + pa_most_slots() * pa_slot_bytes(head_dim);
+}
+
 extern "C" int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
                                     int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
                                     int64_t v_head_stride, int64_t tokens, int64_t kv_tokens, const int32_t* cu_seqlens,
                                     const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads, int32_t kv_heads,
                                     int32_t head_dim, int32_t causal, float sm_scale, void* out, float* lse,
-                                    uint32_t* status, void* stream) {
+                                    uint32_t* work, void* partial, size_t partial_bytes, uint32_t* status, void* stream) {
   PaArgs a = {};
   CUtensorMap mq, mk, mv;
   int rc = pa_common(q, q_token_stride, q_head_stride, tokens, cu_seqlens, batch, num_heads, kv_heads, head_dim, sm_scale,
-                     out, lse, status, a, &mq);
+                     out, lse, work, partial, partial_bytes, kv_tokens, status, a, &mq);
   if (rc != HPC_OK) return rc;
   if (kv_tokens < 0 || kv_tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "kv_tokens out of range");
   if (!cu_seqlens_k && kv_tokens != tokens)
@@ -929,11 +1124,13 @@ extern "C" int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride,
                                           const int32_t* block_table, int32_t max_pages_per_req,
                                           const int32_t* seq_lens, int64_t tokens, const int32_t* cu_seqlens,
                                           int32_t batch, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                          float sm_scale, void* out, float* lse, uint32_t* status, void* stream) {
+                                          float sm_scale, void* out, float* lse, uint32_t* work, void* partial,
+                                          size_t partial_bytes, uint32_t* status, void* stream) {
   PaArgs a = {};
   CUtensorMap mq, mk, mv;
   int rc = pa_common(q, q_token_stride, q_head_stride, tokens, cu_seqlens, batch, num_heads, kv_heads, head_dim, sm_scale,
-                     out, lse, status, a, &mq);
+                     out, lse, work, partial, partial_bytes, static_cast<int64_t>(max_pages_per_req) * page_size, status,
+                     a, &mq);
   if (rc != HPC_OK) return rc;
   if (!k_pages || !v_pages || !block_table || !seq_lens) return fail(HPC_ERR_ARG, "null pointer argument");
   if (kv_dtype != HPC_BF16) return fail(HPC_ERR_DTYPE, "the paged prompt attention reads BF16 caches");

@@ -113,6 +113,78 @@ def test_long(B, lens, Hq, Hkv, D):
         o += x
 
 
+@pytest.mark.parametrize("lens,keys", [((1,), (9000,)), ((16,), (30011,)), ((300, 2, 5), (20000, 700, 1537)),
+                                       ((40, 40, 33, 1), (5000, 129, 0, 12000)), ((1700,), (1700,)), ((2500, 3), (2500, 6001)),
+                                       ((7,) * 9, (3000,) * 9)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (2, 2, 64), (16, 2, 128), (1, 1, 64)])
+def test_cut_along_the_keys(B, lens, keys, Hq, Hkv, D):
+    """Few queries on many keys: units are cut into parts that are joined, the same way every time."""
+    q, k, v = draw(1, sum(lens), Hq, D, scale=2.0), draw(2, sum(keys), Hkv, D), draw(3, sum(keys), Hkv, D)
+    for causal in (True, False):
+        out, lse, st = B.prompt_attention(q, k, v, cu(lens), cu_seqlens_k=cu(keys), causal=causal, return_lse=True)
+        assert int(st.item()) == 0
+        o = p = 0
+        for x, y in zip(lens, keys):
+            check(out[o:o + x], lse[o:o + x], reference(q[o:o + x], k[p:p + y], v[p:p + y], D ** -0.5, causal))
+            o, p = o + x, p + y
+        for _ in range(3):
+            again = B.prompt_attention(q, k, v, cu(lens), cu_seqlens_k=cu(keys), causal=causal, return_lse=True)
+            assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("room", [0, 1, 9, 10 ** 9])
+def test_any_room_for_parts_will_do(B, room):
+    """Through the C call: scratch for no part, for one, for a few, for all."""
+    lens, keys, Hq, Hkv, D = (40, 9), (7000, 4000), 4, 2, 64
+    q, k, v = draw(1, 49, Hq, D), draw(2, 11000, Hkv, D), draw(3, 11000, Hkv, D)
+    full = B._lib.hpc_prompt_attention_partial_bytes(D)
+    slot = 2 * 128 * (D + 2) * 4
+    nbytes = min(16384 + room * slot, full)  # the list of cut units, then the parts
+    partial = torch.full((nbytes + 256,), 255, dtype=torch.uint8, device="cuda")
+    work = torch.zeros(B.PROMPT_WORK_WORDS, dtype=torch.int32, device="cuda")
+    out, lse, st = torch.empty_like(q), torch.empty(49, Hq, device="cuda"), B.new_status("cuda")
+    cq, ck = cu(lens), cu(keys)
+    B._launch("hpc_prompt_attention", q.device, q.data_ptr(), Hq * D, D, k.data_ptr(), Hkv * D, D, v.data_ptr(), Hkv * D, D,
+              49, 11000, cq.data_ptr(), ck.data_ptr(), 2, Hq, Hkv, D, 1, 0.125, out.data_ptr(), lse.data_ptr(),
+              work.data_ptr(), partial.data_ptr(), nbytes, st.data_ptr())
+    assert int(st.item()) == 0 and (partial[nbytes:] == 255).all()
+    o = p = 0
+    for x, y in zip(lens, keys):
+        check(out[o:o + x], lse[o:o + x], reference(q[o:o + x], k[p:p + y], v[p:p + y], 0.125, True))
+        o, p = o + x, p + y
+
+
+@pytest.mark.parametrize("which,at", [("v", 8990), ("v", 100), ("k", 5000)])
+def test_cut_with_values_that_are_not_finite(B, which, at):
+    q, k, v = draw(1, 30, 8, 128), draw(2, 9000, 1, 128), draw(3, 9000, 1, 128)
+    x = {"k": k.clone(), "v": v.clone()}
+    x[which][at, 0, 7] = math.nan
+    out, lse, st = B.prompt_attention(q, x["k"], x["v"], cu([30]), cu_seqlens_k=cu([9000]), return_lse=True)
+    assert int(st.item()) == 0
+    before = max(0, at - 8970)  # queries that do not see it
+    want = reference(q, k, v, 128 ** -0.5, True)
+    check(out[:before], lse[:before], [w[:before] for w in want])
+    seen = out[before:]
+    if which == "v":
+        assert torch.isnan(seen[:, :, 7]).all() and not torch.isnan(seen[:, :, :7]).any()
+        check(out[:, :, 8:], lse, [want[0][:, :, 8:], want[1], want[2][:, :, 8:], want[3]])
+    else:
+        assert torch.isnan(seen).all() and torch.isnan(lse[before:]).all()
+
+
+@pytest.mark.parametrize("P,layout", [(16, "HND"), (64, "NHD"), (128, "HND")])
+def test_cut_paged(B, P, layout):
+    lens, ctx = (3, 64, 1), (20000, 5000, 2047)
+    kp, vp, table, seq, ks, vs = paged(P, lens, ctx, 2, 128, P, layout)
+    q = draw(3, sum(lens), 8, 128)
+    out, lse, st = B.prompt_attention_paged(q, kp, vp, table, seq, cu(lens), kv_layout=layout, return_lse=True)
+    assert int(st.item()) == 0
+    o = 0
+    for r, x in enumerate(lens):
+        check(out[o:o + x], lse[o:o + x], reference(q[o:o + x], ks[r], vs[r], 128 ** -0.5, True))
+        o += x
+
+
 def test_reference_is_the_oracle():
     q, k, v = draw(1, 9, 4, 64), draw(2, 20, 2, 64), draw(3, 20, 2, 64)
     for causal in (True, False):
