@@ -26,7 +26,7 @@
 // longer than a CTA's share of all blocks (few heads, or a few new tokens on a long cache), they are cut into
 // parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second kernel, launched behind
 // this one, joins them (a last part that joined the others by itself took 40 us for 18 parts of a tile: one SM
-// reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 294 us uncut, @@SPLIT@@ us so.
+// reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut, 39 us so.
 // The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
 // (swizzled planes of 64 elements).
 //
@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int64_t length = share > kPaMinPart ? share : kPaMinPart;
     auto cut = [&](int b) -> int32_t {
       const int64_t most = ((b + 1ll) * width + 1) * tokens_per_unit / kPaKeys + 1, least = static_cast<int64_t>(b) * width * tokens_per_unit / kPaKeys;
-      if (a.slots == 0 || most <= length || 2 * least < length) return 1;
+      // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
+      if (a.slots == 0 || 10 * most <= 13 * length || 2 * least < length) return 1;
       const int64_t n = (most + length - 1) / length;
       return static_cast<int32_t>(n < kPaMaxParts ? n : kPaMaxParts);
     };
