@@ -163,13 +163,14 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VfArgs a, i
   };
   // Sum of the weights of [from, stop) (whole warp). Conversions to fp64 and the instructions around them bound
   // this as much as memory does, so whole batches go without tests: fmaxf makes NaN and negative values 0, and
-  // an infinity shows in the sum. Then (`careful`) every value is tested.
+  // an infinity shows in the sum (of q: in the maximum). Then (`careful`) every value is tested.
   bool careful = false;
   auto sum_run = [&](int32_t from, int32_t stop) {
     double sum = 0.0;
     int32_t i = from;
     if (!careful && gone < 0) {
       if (rest) {
+        float top = 0.f;
         for (; i + 32 * kVfBatch <= stop; i += 32 * kVfBatch) {
           float x[kVfBatch], y[kVfBatch];
 #pragma unroll
@@ -182,8 +183,10 @@ __global__ void __launch_bounds__(kVfThreads, 2) verify_kernel(const VfArgs a, i
             const float a = fmaxf(x[k], 0.f), b = fmaxf(y[k], 0.f);
             const double d = static_cast<double>(a) - static_cast<double>(b);
             if (a > b) sum += d;
+            top = fmaxf(top, b);
           }
         }
+        if (top > 3.402823466e38f) sum = top;
       } else {
         for (; i + 32 * kVfBatch <= stop; i += 32 * kVfBatch) {
           float x[kVfBatch];

@@ -115,6 +115,19 @@ def test_values_that_are_no_probabilities_count_as_zero(B, V, bads):
     check(B, x, p, q, u, n, lens)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [700, 40001, 131071])
+def test_an_infinity_of_the_draft_counts_as_zero(B, V, dtype):
+    # Half of the target's mass lies where the draft's value is infinite: the rest there is the target's share.
+    p, q = torch.full((4, 2, V), 2.0**-20, dtype=dtype), torch.full((4, 1, V), 2.0**-19, dtype=dtype)
+    for r, at in enumerate((V // 2, V // 3, 5, V - 1)):
+        p[r, 0, at], q[r, 0, at], p[r, 0, V // 5] = 0.5, float("inf"), 0.25
+    q[:, 0, V // 5] = 2.0**-21  # exact sums: 0.25 - 2^-21 and 0.5 are all that is left
+    x = torch.full((4, 1), V // 7, dtype=torch.int32)
+    for draw in (0.125, 0.375, 0.75):
+        check(B, x, p, q, torch.tensor([[0.9, draw]] * 4))
+
+
 def test_status_bits(B):
     x, p, q, u, n, _ = case(5, 4, 3, 64, torch.float32, agree=0.0)
     u[:] = 0.0
