@@ -602,7 +602,7 @@ HPC_API int hpc_verify_drafts(const int32_t* draft_tokens, const void* target_pr
  * its new columns. A request that grows inside a part-filled page that others hold too (a count above 1
  * after the releases) takes a copy of it first. new_lens 0 ends a request. A length below 0 or beyond
  * the table sets HPC_DEV_BAD_SEQLEN and leaves the row as it is; a held entry outside the pool sets
- * HPC_DEV_BAD_PAGE. move_capacity >= batch; batch <= 8192. */
+ * HPC_DEV_BAD_PAGE. move_capacity >= batch; batch <= 8192; batch * max_pages_per_req <= INT32_MAX. */
 HPC_API int hpc_pages_resize(const int32_t* table_in, int32_t* table_out, int32_t batch, int32_t max_pages_per_req,
                              int32_t page_size, const int32_t* old_lens, const int32_t* new_lens,
                              const int32_t* ref_in, int32_t* ref_out, int32_t num_pages, int32_t* moves,
@@ -612,7 +612,8 @@ HPC_API int hpc_pages_resize(const int32_t* table_in, int32_t* table_out, int32_
  * prompt, requests that leave a batch. Full pages are shared. Of a part-filled last page the first
  * child (lowest r) keeps the page and every other takes a copy. Rows that no child names are released.
  * A parent outside [-1, rows_in) sets HPC_DEV_BAD_INDEX and gives an empty row; a parent with an
- * invalid length sets HPC_DEV_BAD_SEQLEN and gives an empty row. move_capacity >= rows_out; rows <= 8192. */
+ * invalid length sets HPC_DEV_BAD_SEQLEN and gives an empty row. move_capacity >= rows_out; rows <= 8192;
+ * rows * max_pages_per_req <= INT32_MAX. */
 HPC_API int hpc_pages_fork(const int32_t* table_in, const int32_t* lens_in, int32_t rows_in, const int32_t* parents,
                            int32_t* table_out, int32_t* lens_out, int32_t rows_out, int32_t max_pages_per_req,
                            int32_t page_size, const int32_t* ref_in, int32_t* ref_out, int32_t num_pages,

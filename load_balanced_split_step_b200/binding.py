@@ -1106,6 +1106,8 @@ def copy_pages(caches, moves, n_moves, *, status=None):
     status = _status(status, dev)
     if not caches:
         return status
+    if not all(isinstance(t, torch.Tensor) for t in caches):
+        raise HpcError("the caches must be tensors")
     shape, size = caches[0].shape, caches[0].element_size()
     for t in caches:
         _want(t, "cache", t.dtype, dev)

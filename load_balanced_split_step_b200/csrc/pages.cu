@@ -470,8 +470,7 @@ struct PgCaches {
 // Work is (move, cache, 16 KB chunk of the page), dealt over a persistent grid in that order.
 __global__ void __launch_bounds__(kPgCopyThreads)
     pages_copy_kernel(const __grid_constant__ PgCaches caches, int32_t n_caches, int64_t page_vecs, int32_t num_pages,
-                      const int2* __restrict__ moves, const int32_t* __restrict__ n_moves, int32_t capacity,
-                      uint32_t* status) {
+                      const int2* moves, const int32_t* n_moves, int32_t capacity, uint32_t* status) {
   pdl_wait();
   pdl_launch_dependents();
   int32_t n = *n_moves;
@@ -513,6 +512,8 @@ int check_common(const int32_t* table_in, const int32_t* table_out, const int32_
 }
 
 int check_rows(int32_t rows, int32_t max_pages, int32_t page_size) {
+  // the pages that all rows need together are counted in 32 bits
+  if (static_cast<int64_t>(rows) * max_pages > INT32_MAX) return fail(HPC_ERR_SHAPE, "rows x max_pages_per_req exceeds INT32_MAX");
   if (rows > kPgMaxRows) return fail(HPC_ERR_SHAPE, "more than %d rows", kPgMaxRows);
   if (page_size < 1) return fail(HPC_ERR_ARG, "page_size must be >= 1");
   if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX)

@@ -184,36 +184,51 @@ __device__ __noinline__ void pa_row(const PaArgs& a, const PaUnit& x, int32_t to
 #pragma unroll
   for (int e = 0; e < kPer; ++e) qf[e] = __bfloat162float(q[lane + 32 * e]);
   float m = -INFINITY, l = 0.f;
-  for (int32_t j = from; j < vis; ++j) {
-    const __nv_bfloat16 *k, *v;
-    if (kPaged) {
-      int32_t page = a.table[static_cast<int64_t>(x.kv0) * a.max_pages + j / a.P];
-      if (page < 0 || page >= a.num_pages) page = 0;
-      const int64_t at = a.nhd ? (static_cast<int64_t>(page) * a.P + j % a.P) * a.Hkv + x.kvh
-                               : (static_cast<int64_t>(page) * a.Hkv + x.kvh) * a.P + j % a.P;
-      k = a.k + at * D;
-      v = a.v + at * D;
-    } else {
-      k = a.k + (x.kv0 + static_cast<int64_t>(j)) * a.k_token + x.kvh * a.k_head;
-      v = a.v + (x.kv0 + static_cast<int64_t>(j)) * a.v_token + x.kvh * a.v_head;
+  constexpr int kBatch = 8;  // keys loaded together: one at a time waits for memory at every key
+  for (int32_t j0 = from; j0 < vis; j0 += kBatch) {
+    float s[kBatch], vf[kBatch][kPer];
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int32_t j = j0 + n < vis ? j0 + n : vis - 1;
+      const __nv_bfloat16 *k, *v;
+      if (kPaged) {
+        int32_t page = a.table[static_cast<int64_t>(x.kv0) * a.max_pages + j / a.P];
+        if (page < 0 || page >= a.num_pages) page = 0;
+        const int64_t at = a.nhd ? (static_cast<int64_t>(page) * a.P + j % a.P) * a.Hkv + x.kvh
+                                 : (static_cast<int64_t>(page) * a.Hkv + x.kvh) * a.P + j % a.P;
+        k = a.k + at * D;
+        v = a.v + at * D;
+      } else {
+        k = a.k + (x.kv0 + static_cast<int64_t>(j)) * a.k_token + x.kvh * a.k_head;
+        v = a.v + (x.kv0 + static_cast<int64_t>(j)) * a.v_token + x.kvh * a.v_head;
+      }
+      s[n] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        s[n] = fmaf(qf[e], __bfloat162float(k[lane + 32 * e]), s[n]);
+        vf[n][e] = __bfloat162float(v[lane + 32 * e]);
+      }
     }
-    float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) s = fmaf(qf[e], __bfloat162float(k[lane + 32 * e]), s);
+    for (int n = 0; n < kBatch; ++n) {
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (s > m) {
-      const float shrink = m == -INFINITY ? 0.f : ex2((m - s) * a.scale_log2);
-      l *= shrink;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = m == -INFINITY ? o[e] : o[e] * shrink;
-      m = s;
+      for (int w = 16; w > 0; w >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], w);
     }
-    if (s == -INFINITY) continue;  // no weight
-    const float p = ex2((s - m) * a.scale_log2);
-    l += p;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = fmaf(p, __bfloat162float(v[lane + 32 * e]), o[e]);
+    for (int n = 0; n < kBatch; ++n) {
+      if (j0 + n >= vis || s[n] == -INFINITY) continue;  // no weight
+      if (s[n] > m) {
+        const float shrink = m == -INFINITY ? 0.f : ex2((m - s[n]) * a.scale_log2);
+        l *= shrink;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[e] = m == -INFINITY ? o[e] : o[e] * shrink;
+        m = s[n];
+      }
+      const float p = ex2((s[n] - m) * a.scale_log2);
+      l += p;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = fmaf(p, vf[n][e], o[e]);
+    }
   }
   if (slot) {
 #pragma unroll
@@ -587,6 +602,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // ------------------------------------------------------------------ units and loads
       uint32_t fill = 0;  // ring fills so far
       int32_t n_unit = 0, n_q = 0;
+      // Where the last lookup ended: this CTA's units come in order, so that within a bucket the next one
+      // goes on from there (a batch of thousands of sequences is gone through once for each bucket).
+      int32_t last_b = -1, last_s0 = 0, last_sum = 0;
       for (bool begun = false;; begun = true) {
         int64_t u = blockIdx.x;
         if (begun) {
@@ -607,7 +625,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           x.part = tile - sh.base[b] - rank * parts;
           x.slot = parts > 1 ? static_cast<int32_t>(u) : 0;
           // sequence: prefix of the tiles that each has in the bucket
-          for (int32_t s0 = 0; s0 < a.batch; s0 += 32) {
+          if (b != last_b) last_b = b, last_s0 = last_sum = 0;
+          rank -= last_sum;
+          for (int32_t s0 = last_s0; s0 < a.batch; s0 += 32) {
             const int32_t s = s0 + lane;
             int32_t q0 = 0, q1 = 0, k0 = 0, keys = 0, lo = 0, hi = 0, from = 0, n = 0;
             if (s < a.batch) {
@@ -657,7 +677,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               }
               break;
             }
-            rank -= __shfl_sync(0xffffffffu, inc, 31);
+            const int32_t sum = __shfl_sync(0xffffffffu, inc, 31);
+            rank -= sum;
+            last_sum += sum;
+            last_s0 = s0 + 32;
           }
         }
         if (x.valid && x.part > 0 && x.blocks[0] == 0 && x.blocks[1] == 0) continue;  // fewer parts than the bucket's
@@ -1024,11 +1047,11 @@ size_t pa_most_slots() {
   return n < kPaCuts ? n : kPaCuts;
 }
 
-// What both entry points check of the queries and the shape; fills the common arguments and q's map.
+// What both entry points check of the queries and the shape; fills the common arguments.
 int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t tokens, const int32_t* cu_seqlens,
               int32_t batch, int32_t num_heads, int32_t kv_heads, int32_t head_dim, float sm_scale, void* out,
               float* lse, uint32_t* work, void* partial, size_t partial_bytes, int64_t max_keys, uint32_t* status,
-              PaArgs& a, CUtensorMap* map) {
+              PaArgs& a) {
   if (tokens < 0 || tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "tokens out of range");
   if (!cu_seqlens || !status || !work || (tokens > 0 && (!q || !out)) || (partial_bytes > 0 && !partial))
     return fail(HPC_ERR_ARG, "null pointer argument");
@@ -1065,7 +1088,11 @@ int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int6
   if (!aligned16(q) || !aligned16(out)) return fail(HPC_ERR_ALIGN, "q and out must be 16-byte aligned");
   if (q_token_stride % 8 || q_head_stride % 8 || q_token_stride < 0 || q_head_stride < 0)
     return fail(HPC_ERR_ALIGN, "strides must be multiples of 8 elements");
-  return pa_packed_map(map, q, tokens, num_heads, head_dim, q_token_stride, q_head_stride, g, kPaRows / g);
+  return HPC_OK;
+}
+
+int pa_query_map(CUtensorMap* map, const PaArgs& a, int32_t head_dim) {
+  return pa_packed_map(map, a.q, a.tokens, a.Hq, head_dim, a.q_token, a.q_head, a.group, kPaRows / a.group);
 }
 
 }  // namespace
@@ -1087,7 +1114,7 @@ extern "C" int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64
   PaArgs a = {};
   CUtensorMap mq, mk, mv;
   int rc = pa_common(q, q_token_stride, q_head_stride, tokens, cu_seqlens, batch, num_heads, kv_heads, head_dim, sm_scale,
-                     out, lse, work, partial, partial_bytes, kv_tokens, status, a, &mq);
+                     out, lse, work, partial, partial_bytes, kv_tokens, status, a);
   if (rc != HPC_OK) return rc;
   if (kv_tokens < 0 || kv_tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "kv_tokens out of range");
   if (!cu_seqlens_k && kv_tokens != tokens)
@@ -1107,6 +1134,7 @@ extern "C" int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64
   a.v_token = v_token_stride;
   a.v_head = v_head_stride;
   a.causal = causal != 0;
+  if ((rc = pa_query_map(&mq, a, head_dim)) != HPC_OK) return rc;
   if (kv_tokens > 0) {
     if ((rc = pa_packed_map(&mk, k, kv_tokens, kv_heads, head_dim, k_token_stride, k_head_stride, 1, kPaKeys)) != HPC_OK)
       return rc;
@@ -1131,7 +1159,7 @@ extern "C" int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride,
   CUtensorMap mq, mk, mv;
   int rc = pa_common(q, q_token_stride, q_head_stride, tokens, cu_seqlens, batch, num_heads, kv_heads, head_dim, sm_scale,
                      out, lse, work, partial, partial_bytes, static_cast<int64_t>(max_pages_per_req) * page_size, status,
-                     a, &mq);
+                     a);
   if (rc != HPC_OK) return rc;
   if (!k_pages || !v_pages || !block_table || !seq_lens) return fail(HPC_ERR_ARG, "null pointer argument");
   if (kv_dtype != HPC_BF16) return fail(HPC_ERR_DTYPE, "the paged prompt attention reads BF16 caches");
@@ -1156,6 +1184,7 @@ extern "C" int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride,
   const uint64_t dims[4] = {D, a.nhd ? H : P, a.nhd ? P : H, static_cast<uint64_t>(num_pages)};
   const uint64_t strides[3] = {D * 2, D * 2 * dims[1], D * 2 * H * P};
   const uint32_t box[4] = {64, a.nhd ? 1u : static_cast<uint32_t>(P), a.nhd ? static_cast<uint32_t>(P) : 1u, 1};
+  if ((rc = pa_query_map(&mq, a, head_dim)) != HPC_OK) return rc;
   if ((rc = pa_map(&mk, k_pages, dims, strides, box)) != HPC_OK) return rc;
   if ((rc = pa_map(&mv, v_pages, dims, strides, box)) != HPC_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

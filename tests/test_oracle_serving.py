@@ -131,6 +131,9 @@ def test_host_checks_of_the_page_calls(B):
     assert fork(rows=0) == B.HPC_ERR_ARG and fork(cap=1) == B.HPC_ERR_CAPACITY
     assert lib.hpc_pages_compact(w, w, 2, 3, w, w, 10, None, w, 5, w, w, None) == B.HPC_ERR_ARG
     assert lib.hpc_pages_compact(w, w, 2, 3, w, w, 10, w, w, 4, w, w, None) == B.HPC_ERR_CAPACITY
+    assert resize(batch=4096, pages=1 << 20, P=1, cap=4096) == B.HPC_ERR_SHAPE
+    assert lib.hpc_pages_fork(w, w, 4096, w, ctypes.c_void_p(512), ctypes.c_void_p(512), 2, 1 << 20, 1, w, w, 10, w, 2, w, w,
+                              None) == B.HPC_ERR_SHAPE
     ptrs = (ctypes.c_void_p * 2)(256, 264)
     assert lib.hpc_pages_copy(None, 1, 16, 4, w, 1, w, w, None) == B.HPC_ERR_ARG
     assert lib.hpc_pages_copy(ptrs, 1, 24, 4, w, 1, w, w, None) == B.HPC_ERR_SHAPE
@@ -156,3 +159,33 @@ def test_host_checks_of_verify_and_prologue(B):
     assert pro(qkv=None) == pro(cu=None) == pro(tokens=-1) == pro(theta=0.0) == pro(kv=B.HPC_E4M3) == B.HPC_ERR_ARG
     assert pro(kv=B.HPC_FP32) == B.HPC_ERR_DTYPE and pro(D=96) == pro(heads=7) == pro(tokens=1 << 31) == B.HPC_ERR_SHAPE
     assert pro(q_out=ctypes.c_void_p(264)) == B.HPC_ERR_ALIGN and pro(tokens=0) == B.HPC_OK
+
+
+def test_host_checks_of_prompt_attention(B):
+    w, odd = ctypes.c_void_p(256), ctypes.c_void_p(264)
+    lib = B._lib
+
+    def packed(q=w, k=w, v=w, stride=1024, kstride=256, tokens=4, kv=4, cu=w, cu_k=None, batch=2, H=8, Hkv=2, D=128,
+               scale=0.1, out=w, work=w, part=None, room=0):
+        return lib.hpc_prompt_attention(q, stride, D, k, kstride, D, v, kstride, D, tokens, kv, cu, cu_k, batch, H, Hkv, D, 1,
+                                        scale, out, None, work, part, room, w, None)
+
+    for bad in (dict(q=None), dict(k=None), dict(v=None), dict(cu=None), dict(out=None), dict(work=None), dict(room=64),
+                dict(tokens=-1), dict(kv=-1, cu_k=w), dict(kv=5), dict(batch=0), dict(H=0), dict(Hkv=0), dict(scale=0.0),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(tokens=1 << 31)):
+        assert packed(**bad) == B.HPC_ERR_ARG, bad
+    for bad in (dict(H=7), dict(H=6), dict(H=32), dict(D=96), dict(D=256)):
+        assert packed(**bad) == B.HPC_ERR_SHAPE, bad
+    for bad in (dict(q=odd), dict(out=odd), dict(part=odd, room=64), dict(stride=1028)):
+        assert packed(**bad) == B.HPC_ERR_ALIGN, bad
+    assert packed(tokens=0, kv=0, q=None, out=None, k=None, v=None) == B.HPC_OK  # nothing to do
+
+    def paged(k=w, kv=B.HPC_BF16, lay=B.HPC_HND, N=4, P=16, table=w, M=3, lens=w, tokens=0):
+        return lib.hpc_prompt_attention_paged(w, 1024, 128, k, w, kv, lay, N, P, table, M, lens, tokens, w, 2, 8, 2, 128, 0.1,
+                                              w, None, w, None, 0, w, None)
+
+    assert paged(k=None) == paged(table=None) == paged(lens=None) == paged(lay=2) == paged(N=0) == paged(M=0) == B.HPC_ERR_ARG
+    assert paged(kv=B.HPC_E4M3) == B.HPC_ERR_DTYPE
+    assert paged(P=8) == paged(P=48) == paged(P=256) == paged(M=1 << 28) == B.HPC_ERR_SHAPE
+    assert paged(k=odd) == B.HPC_ERR_ALIGN and paged() == B.HPC_OK
+    assert lib.hpc_prompt_attention_partial_bytes(96) == 0 and lib.hpc_prompt_attention_partial_bytes(64) > 0
