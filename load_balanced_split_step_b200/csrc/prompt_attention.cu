@@ -22,13 +22,21 @@
 // taken over the unrounded values.
 //
 // Persistent CTAs (one per SM) take units longest first from a counter: units are put in 64 buckets by the number
-// of keys they reach, in a table that every CTA builds from cu_seqlens at the start. Where a bucket's units are
-// longer than a CTA's share of all blocks (few heads, or a few new tokens on a long cache), they are cut into
-// parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second kernel, launched behind
-// this one, joins them (a last part that joined the others by itself took 40 us for 18 parts of a tile: one SM
-// reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut, 39 us so.
+// of keys they reach, in a table that every CTA builds from cu_seqlens at the start. (Where there is a CTA for every
+// unit they are dealt as they come: without the table a prompt of 200 tokens takes 11.3 us instead of 12.5.)
+// Where a bucket's units are longer than a CTA's share of all blocks (few heads, or a few new tokens on a long
+// cache), they are cut into parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second
+// kernel, launched behind this one, joins them (a last part that joined the others by itself took 40 us for 18 parts
+// of a tile: one SM reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut,
+// 39 us so. Parts of less than 6 blocks cost more in the joining than they save (sweep of 4, 6, 8, 12).
 // The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
-// (swizzled planes of 64 elements).
+// (swizzled planes of 64 elements). The next unit's Q has to wait for its place, and comes as far as L2 meanwhile
+// (its arrival after that took 3000 cycles, now 1400).
+//
+// Bound by the tensor cores, and in long prompts by power: 8192 tokens of 64/8 heads of 128 take 840 us cold
+// (1.31 PFLOP/s of the triangle's products) and 955 us in a row (1000 W, 1.4 GHz), where a large library product
+// falls to 1.37 PFLOP/s. Short prompts are bound by the softmax warps' own chain (scores, exponentials, epilogue: 7300
+// cycles per unit of one block): 64 prompts of 128 tokens take 92 us, twice what their bytes would.
 //
 // Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 issues the products with
 // K, warp 10 those with V, warp 9 looks up units and loads, warp 11 checks V. A softmax thread holds the 128
@@ -104,6 +112,7 @@ struct PaArgs {
   int64_t tokens, kv_tokens, max_pages;
   float scale_log2, scale;
   int32_t batch, Hq, Hkv, group, causal, P, num_pages, nhd, slots;
+  int32_t unsorted;  // a CTA for every unit: they are dealt as they come
 };
 
 struct PaBars {
@@ -150,12 +159,12 @@ __device__ __forceinline__ bool pa_sequence(const PaArgs& a, bool paged, int32_t
   return ok;
 }
 
-// The sequence's token tiles on the cost axis [lo, hi): a tile costs the tiles' worth of keys it reaches.
-__device__ __forceinline__ void pa_span(const PaArgs& a, int32_t q0, int32_t q1, int32_t keys, int32_t tile_tokens,
-                                        int32_t& lo, int32_t& hi) {
+// The sequence's units on the cost axis [lo, hi): a unit of 2^shift tokens costs the units' worth of keys it reaches.
+__device__ __forceinline__ void pa_span(const PaArgs& a, int32_t q0, int32_t q1, int32_t keys, int shift, int32_t& lo,
+                                        int32_t& hi) {
   const int32_t n = q1 - q0, before = a.causal ? (keys > n ? keys - n : 0) : keys;
-  lo = before / tile_tokens;
-  hi = lo + (n + tile_tokens - 1) / tile_tokens;
+  lo = before >> shift;
+  hi = lo + ((n + (1 << shift) - 1) >> shift);
 }
 
 // One step of a transposition over lanes: the upper lane's `a` and the lower lane's `b` change places.
@@ -259,7 +268,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + L::kOffRing;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t tokens_per_tile = kPaRows / a.group, tokens_per_unit = 2 * tokens_per_tile;
+  const int group_shift = 31 - __clz(a.group), unit_shift = 8 - group_shift;  // 1, 2, 4 or 8 heads
+  const int32_t tokens_per_unit = 1 << unit_shift, tokens_per_tile = tokens_per_unit / 2;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
   if (threadIdx.x == 0) {
@@ -300,79 +310,96 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the table of units: 64 buckets of the cost axis
-  {
-    int32_t span = 0, bad = 0;
-    int64_t rows = 0;  // keys that the tiles reach
-    for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
-      int32_t q0, q1, k0, keys, lo, hi;
-      bad |= !pa_sequence(a, kPaged, s, q0, q1, k0, keys);
-      pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
-      if (hi > span) span = hi;
-      rows += (static_cast<int64_t>(hi) * (hi + 1) - static_cast<int64_t>(lo) * (lo + 1)) / 2 * tokens_per_unit;
-    }
-    atomicMax(&sh.span, span);
-    if (rows > 0) atomicAdd(&sh.blocks, static_cast<unsigned long long>(rows / kPaKeys + 1));
-    if (bad) sh.bad = 1;
-    __syncthreads();
-    if (threadIdx.x == 0 && sh.bad && blockIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
-  }
-  const int32_t width = (sh.span + kPaBuckets - 1) / kPaBuckets > 0 ? (sh.span + kPaBuckets - 1) / kPaBuckets : 1;
-  for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
-    int32_t q0, q1, k0, keys, lo, hi;
-    pa_sequence(a, kPaged, s, q0, q1, k0, keys);
-    pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
-    if (hi > lo) {
-      atomicAdd(&sh.hist[hi / width], 1);
-      atomicAdd(&sh.rem[hi / width], hi % width);
-      atomicAdd(&sh.hist[lo / width], -1);
-      atomicAdd(&sh.rem[lo / width], -(lo % width));
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // longest first: lane l holds the buckets 63 - 2 l and 62 - 2 l
-    const int b0 = kPaBuckets - 1 - 2 * lane, b1 = b0 - 1;
-    auto scan = [&](int32_t v) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      return v;
-    };
-    const int32_t h0 = sh.hist[b0], h1 = sh.hist[b1];
-    const int32_t above = sh.hist[kPaBuckets] + scan(h0 + h1) - h0 - h1;  // sequences that end past bucket b0
-    const int32_t c0 = above * width + sh.rem[b0], c1 = (above + h0) * width + sh.rem[b1];
-    // Parts per tile: about a CTA's share of all blocks each, as long as the scratch has a place for them. The
-    // buckets that are cut come first, so that a part's number is its place.
-    const int64_t all = static_cast<int64_t>(sh.blocks) * a.Hkv, share = (all + gridDim.x - 1) / gridDim.x;
-    const int64_t length = share > kPaMinPart ? share : kPaMinPart;
-    auto cut = [&](int b) -> int32_t {
-      const int64_t most = ((b + 1ll) * width + 1) * tokens_per_unit / kPaKeys + 1, least = static_cast<int64_t>(b) * width * tokens_per_unit / kPaKeys;
-      // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
-      if (a.slots == 0 || 10 * most <= 13 * length || 2 * least < length) return 1;
-      const int64_t n = (most + length - 1) / length;
-      return static_cast<int32_t>(n < kPaMaxParts ? n : kPaMaxParts);
-    };
-    int32_t p0 = cut(b0), p1 = cut(b1);
-    const int64_t room = a.slots / a.Hkv;
+  // ---- the table of units: buckets of 2^bucket units of the cost axis, 64 at most
+  int bucket = 0;
+  uint32_t units = 0;
+  if (!a.unsorted) {
+    int32_t lo0 = 0, hi0 = 0;  // the thread's first sequence
     {
-      const int32_t end = scan(c0 * p0 + c1 * p1);
-      if (end - c1 * p1 > room) p0 = 1;
-      if (end > room) p1 = 1;
+      int32_t span = 0, bad = 0;
+      int64_t rows = 0;  // keys that the units reach
+      for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
+        int32_t q0, q1, k0, keys, lo, hi;
+        bad |= !pa_sequence(a, kPaged, s, q0, q1, k0, keys);
+        pa_span(a, q0, q1, keys, unit_shift, lo, hi);
+        if (hi > span) span = hi;
+        rows += ((static_cast<int64_t>(hi) * (hi + 1) - static_cast<int64_t>(lo) * (lo + 1)) / 2) << unit_shift;
+        if (s == static_cast<int32_t>(threadIdx.x)) lo0 = lo, hi0 = hi;
+      }
+      if (span > 0) atomicMax(&sh.span, span);
+      if (rows > 0 && a.slots > 0) atomicAdd(&sh.blocks, static_cast<unsigned long long>(rows / kPaKeys + 1));
+      if (bad) sh.bad = 1;
+      __syncthreads();
+      if (threadIdx.x == 0 && sh.bad && blockIdx.x == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
     }
-    const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
-    sh.parts[b0] = p0;
-    sh.parts[b1] = p1;
-    sh.count[b0] = n0;
-    sh.count[b1] = n1;
-    sh.base[b0] = upto - n0 - n1;
-    sh.base[b1] = upto - n1;
-    if (lane == 31) sh.tiles = upto;
+    const int32_t per_bucket = (sh.span + kPaBuckets - 1) / kPaBuckets;
+    bucket = per_bucket > 1 ? 32 - __clz(per_bucket - 1) : 0;
+    for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
+      int32_t lo = lo0, hi = hi0;
+      if (s >= kPaThreads) {
+        int32_t q0, q1, k0, keys;
+        pa_sequence(a, kPaged, s, q0, q1, k0, keys);
+        pa_span(a, q0, q1, keys, unit_shift, lo, hi);
+      }
+      if (hi > lo) {
+        const int32_t mask = (1 << bucket) - 1;
+        atomicAdd(&sh.hist[hi >> bucket], 1);
+        atomicAdd(&sh.rem[hi >> bucket], hi & mask);
+        atomicAdd(&sh.hist[lo >> bucket], -1);
+        atomicAdd(&sh.rem[lo >> bucket], -(lo & mask));
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // longest first: lane l holds the buckets 63 - 2 l and 62 - 2 l
+      const int b0 = kPaBuckets - 1 - 2 * lane, b1 = b0 - 1;
+      auto scan = [&](int32_t v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        return v;
+      };
+      const int32_t h0 = sh.hist[b0], h1 = sh.hist[b1];
+      const int32_t above = sh.hist[kPaBuckets] + scan(h0 + h1) - h0 - h1;  // sequences that end past bucket b0
+      const int32_t c0 = (above << bucket) + sh.rem[b0], c1 = ((above + h0) << bucket) + sh.rem[b1];
+      int32_t p0 = 1, p1 = 1;
+      if (a.slots > 0) {
+        // Parts per unit: about a CTA's share of all blocks each, as long as the scratch has a place for them. The
+        // buckets that are cut come first, so that a part's number is its place.
+        const float share = static_cast<float>(sh.blocks) * a.Hkv / gridDim.x;  // the same in every CTA
+        const int32_t length = share > kPaMinPart ? static_cast<int32_t>(fminf(ceilf(share), 1e9f)) : kPaMinPart;
+        auto cut = [&](int b) -> int32_t {
+          const int64_t most = (((static_cast<int64_t>(b + 1) << bucket) + 1) << unit_shift) / kPaKeys + 1,
+                        least = ((static_cast<int64_t>(b) << bucket) << unit_shift) / kPaKeys;
+          // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
+          if (10 * most <= 13ll * length || 2 * least < length) return 1;
+          const float n = ceilf(static_cast<float>(most) / static_cast<float>(length));
+          return n < kPaMaxParts ? static_cast<int32_t>(n) : kPaMaxParts;
+        };
+        p0 = cut(b0), p1 = cut(b1);
+        const int32_t room = a.slots / a.Hkv, end = scan(c0 * p0 + c1 * p1);
+        if (end - c1 * p1 > room) p0 = 1;
+        if (end > room) p1 = 1;
+      }
+      const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
+      sh.parts[b0] = p0;
+      sh.parts[b1] = p1;
+      sh.count[b0] = n0;
+      sh.count[b1] = n1;
+      sh.base[b0] = upto - n0 - n1;
+      sh.base[b1] = upto - n1;
+      if (lane == 31) sh.tiles = upto;
+    }
+    __syncthreads();
+    units = static_cast<uint32_t>(sh.tiles) * a.Hkv;  // fewer than rows of q
+  } else if (blockIdx.x == 0) {
+    for (int32_t s = threadIdx.x; s < a.batch; s += kPaThreads) {
+      int32_t q0, q1, k0, keys;
+      if (!pa_sequence(a, kPaged, s, q0, q1, k0, keys)) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
+    }
   }
-  __syncthreads();
-  const int64_t units = static_cast<int64_t>(sh.tiles) * a.Hkv;
   bool ok = true;
   uint32_t err = 0;
   auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
@@ -390,8 +417,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int row = threadIdx.x & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t p_at = lanes + 128 + 64 * t, o_at = lanes + 256 + 128 * t;
-    const int32_t tok = t * tokens_per_tile + row / a.group;
-    const int group_shift = 31 - __clz(a.group);
+    const int32_t tok = t * tokens_per_tile + (row >> group_shift);
+    const int32_t tok_low = t * tokens_per_tile + ((row & ~31) >> group_shift);  // of the warp
     const float c = a.scale_log2;
     uint32_t done = 0;  // blocks of this tile so far
     uint32_t fill = 0;  // ring stages of the units before
@@ -404,11 +431,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (!x.valid) break;
       const int nb = t == 0 ? x.blocks[0] : x.blocks[1];
       const int nb_unit = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
-      // keys this row sees; fewest of the tile's rows
-      int32_t vis = a.causal ? x.vis + tok : x.keys;
-      if (vis > x.keys) vis = x.keys;
-      int32_t vis_min = a.causal ? x.vis + t * tokens_per_tile : x.keys;
-      if (vis_min > x.keys) vis_min = x.keys;
+      // keys this row sees; fewest of the warp's rows
+      const int32_t vis = a.causal ? min(x.vis + tok, x.keys) : x.keys;
+      const int32_t vis_low = a.causal ? min(x.vis + tok_low, x.keys) : x.keys;
       float m = -INFINITY, l = 0.f;
       for (int j = x.from; j < x.from + nb && ok; ++j) {
         wait(sh.bars.s_full[t], done & 1);
@@ -420,11 +445,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(sh.bars.s_read[t]));  // S is free for the other tile
-        const bool masked = (j + 1) * kPaKeys > vis_min;
-        if (masked) {
-          const int32_t lim = vis - j * kPaKeys;
+        if ((j + 1) * kPaKeys > vis_low) {
+          const int32_t lim = vis - j * kPaKeys, low = vis_low - j * kPaKeys;
+          // groups of 32 keys that the whole warp sees stay as they are
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = i < lim ? v[i] : -INFINITY;
+          for (int h = 0; h < kPaKeys / 32; ++h) {
+            if (32 * (h + 1) > low) {
+#pragma unroll
+              for (int i = 32 * h; i < 32 * (h + 1); ++i) v[i] = i < lim ? v[i] : -INFINITY;
+            }
+          }
         }
         float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
 #pragma unroll
@@ -591,7 +621,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (there[k]) *reinterpret_cast<uint4*>(dst[k] + c0) = w[k];
       }
       if (a.lse && live)
-        a.lse[static_cast<int64_t>(x.q0 + tok) * a.Hq + x.kvh * a.group + row % a.group] =
+        a.lse[static_cast<int64_t>(x.q0 + tok) * a.Hq + x.kvh * a.group + (row & (a.group - 1))] =
             l > 0.f || l != l ? m * a.scale + logf(l) : -INFINITY;
       tc_fence_before();
     }
@@ -605,36 +635,47 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       // Where the last lookup ended: this CTA's units come in order, so that within a bucket the next one
       // goes on from there (a batch of thousands of sequences is gone through once for each bucket).
       int32_t last_b = -1, last_s0 = 0, last_sum = 0;
+      uint32_t dealt = blockIdx.x;
       for (bool begun = false;; begun = true) {
-        int64_t u = blockIdx.x;
-        if (begun) {
-          if (lane == 0) u = static_cast<int64_t>(gridDim.x) + atomicAdd(a.work, 1u);
+        uint32_t u = blockIdx.x;
+        if (a.unsorted) {
+          u = dealt;
+          dealt += gridDim.x;  // none is left, unless the lengths overlap
+        } else if (begun) {
+          if (lane == 0) u = gridDim.x + atomicAdd(a.work, 1u);
           u = __shfl_sync(0xffffffffu, u, 0);
         }
         PaUnit x = {};
-        x.valid = u < units;
-        if (x.valid) {
-          const int32_t tile = static_cast<int32_t>(u / a.Hkv);
-          x.kvh = static_cast<int32_t>(u - static_cast<int64_t>(tile) * a.Hkv);
-          // bucket: the one with base <= tile < base + count
-          uint32_t m0 = __ballot_sync(0xffffffffu, tile >= sh.base[lane] && tile < sh.base[lane] + sh.count[lane]);
-          uint32_t m1 = __ballot_sync(0xffffffffu, tile >= sh.base[lane + 32] && tile < sh.base[lane + 32] + sh.count[lane + 32]);
-          const int b = m0 ? __ffs(m0) - 1 : 32 + __ffs(m1) - 1;
-          const int32_t parts = sh.parts[b];
-          int32_t rank = (tile - sh.base[b]) / parts;
-          x.part = tile - sh.base[b] - rank * parts;
-          x.slot = parts > 1 ? static_cast<int32_t>(u) : 0;
-          // sequence: prefix of the tiles that each has in the bucket
-          if (b != last_b) last_b = b, last_s0 = last_sum = 0;
+        if (a.unsorted || u < units) {
+          const int32_t tile = static_cast<int32_t>(u / static_cast<uint32_t>(a.Hkv));
+          x.kvh = static_cast<int32_t>(u) - tile * a.Hkv;
+          int32_t rank = tile, parts = 1, bucket_lo = 0, bucket_hi = INT32_MAX;
+          if (!a.unsorted) {
+            // bucket: the one with base <= tile < base + count
+            uint32_t m0 = __ballot_sync(0xffffffffu, tile >= sh.base[lane] && tile < sh.base[lane] + sh.count[lane]);
+            uint32_t m1 = __ballot_sync(0xffffffffu, tile >= sh.base[lane + 32] && tile < sh.base[lane + 32] + sh.count[lane + 32]);
+            const int b = m0 ? __ffs(m0) - 1 : 32 + __ffs(m1) - 1;
+            parts = sh.parts[b];
+            rank -= sh.base[b];
+            if (parts > 1) {
+              x.part = rank % parts;
+              rank /= parts;
+              x.slot = static_cast<int32_t>(u);
+            }
+            bucket_lo = b << bucket;
+            bucket_hi = (b + 1) << bucket;
+            if (b != last_b) last_b = b, last_s0 = last_sum = 0;
+          }
           rank -= last_sum;
+          // sequence: prefix of the tiles that each has in the bucket
           for (int32_t s0 = last_s0; s0 < a.batch; s0 += 32) {
             const int32_t s = s0 + lane;
             int32_t q0 = 0, q1 = 0, k0 = 0, keys = 0, lo = 0, hi = 0, from = 0, n = 0;
             if (s < a.batch) {
               pa_sequence(a, kPaged, s, q0, q1, k0, keys);
-              pa_span(a, q0, q1, keys, tokens_per_unit, lo, hi);
-              from = lo > b * width ? lo : b * width;
-              const int32_t to = hi < (b + 1) * width ? hi : (b + 1) * width;
+              pa_span(a, q0, q1, keys, unit_shift, lo, hi);
+              from = max(lo, bucket_lo);
+              const int32_t to = min(hi, bucket_hi);
               n = to > from ? to - from : 0;
             }
             int32_t inc = n;
@@ -645,6 +686,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             }
             const uint32_t hit = __ballot_sync(0xffffffffu, rank < inc);
             if (hit) {
+              x.valid = 1;
               const int w = __ffs(hit) - 1;
               const int32_t i = __shfl_sync(0xffffffffu, from - lo + rank - (inc - n), w);
               q0 = __shfl_sync(0xffffffffu, q0, w);
@@ -672,7 +714,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               x.from = x.part * length;
               for (int t = 0; t < 2; ++t) {
                 const int32_t have = x.blocks[t], left = have - x.from;
-                x.parts[t] = length > 0 ? (have + length - 1) / length : 0;
+                x.parts[t] = parts > 1 ? (have + length - 1) / length : (have > 0 ? 1 : 0);
                 x.blocks[t] = left < 0 ? 0 : (left < length ? left : length);
               }
               break;
@@ -698,7 +740,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!x.valid) break;
         const int nb = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
         if (nb == 0) continue;  // no keys: the epilogue writes zeros
-        // Q, once the products of the unit before have read theirs
+        // Q, once the products of the unit before have read theirs; until then it comes as far as L2
+        if (n_q > 0 && lane < 2 * L::kPlanes)
+          tma_prefetch_4d(&tm_q, 64 * (lane / 2), x.kvh * a.group, x.q0 + (lane & 1) * tokens_per_tile, 0);
         if (n_q > 0) wait(sh.bars.q_free, (n_q - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -1014,7 +1058,7 @@ int pa_packed_map(CUtensorMap* map, const void* base, int64_t tokens, int32_t he
 }
 
 template <int D, bool kPaged>
-int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PaArgs& a, cudaStream_t stream) {
+int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, PaArgs a, cudaStream_t stream) {
   using L = PaLayout<D>;
   static int configured[64] = {0};
   int dev = 0;
@@ -1030,6 +1074,7 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
   const int64_t per_unit = 2 * kPaRows / a.group;
   const int64_t most = (a.tokens / per_unit + (a.batch < a.tokens ? a.batch : a.tokens)) * a.Hkv;
   const int grid = a.slots > 0 ? sms : static_cast<int>(most < sms ? most : sms);
+  a.unsorted = a.slots == 0 && most <= sms;
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kPaThreads), static_cast<size_t>(L::kBytes), stream, q, k, v, a);
   if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_attention_kernel: %s", cudaGetErrorString(e));
   const int rc = check_launch("prompt_attention_kernel");
