@@ -28,7 +28,8 @@
 // cache), they are cut into parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second
 // kernel, launched behind this one, joins them (a last part that joined the others by itself took 40 us for 18 parts
 // of a tile: one SM reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut,
-// 39 us so. Parts of less than 6 blocks cost more in the joining than they save (sweep of 4, 6, 8, 12).
+// 39 us so. A part has 6 blocks at least: of 2, 3, 4, 6 and 9
+// that loses least over nine shapes (mixed lengths on 9000 keys 53 us at 2, 47 at 6, 41 at 9; 800 on 1800 keys 22, 25, 29).
 // The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
 // (swizzled planes of 64 elements). The next unit's Q has to wait for its place, and comes as far as L2 meanwhile
 // (its arrival after that took 3000 cycles, now 1400).
@@ -61,7 +62,7 @@ constexpr uint32_t kPaCols = 512;       // S 0, P_A 128, P_B 192, O_A 256, O_B 3
 constexpr float kPaMove = 8.f;
 constexpr int kPaSplit = 2;               // P is handed over in two parts: after 64 keys, and whole
 constexpr int kPaStages64 = 8, kPaStages128 = 5;
-constexpr int kPaMinPart = 6;           // blocks: a shorter part costs more in the joining than it saves
+constexpr int kPaMinPart = 6;           // blocks: joining costs more than shorter parts save
 constexpr int kPaMaxParts = 32;
 constexpr int kPaCuts = 512;            // cut units that the scratch can describe, ahead of the slots
 

@@ -407,6 +407,70 @@ def test_streams_and_graphs(B):
         assert torch.equal(out[:e], B.prompt_attention(q, k, v, lens)[0][:e]) and not out[e:].any()
 
 
+def test_cut_on_streams_and_in_a_graph(B):
+    # 40 queries on 5000 keys of 2 kv heads are cut; each call has counters and scratch of its own.
+    cq, ck = cu([40]), cu([5000])
+    q, k, v = draw(1, 40, 8, 128), draw(2, 6000, 2, 128), draw(3, 6000, 2, 128)
+    want = B.prompt_attention(q, k, v, cq, cu_seqlens_k=ck)[0]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs += [B.prompt_attention(q, k, v, cq, cu_seqlens_k=ck)[0] for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    out, other, st = torch.zeros_like(q), torch.zeros_like(q), B.new_status("cuda")
+    graphs = []
+    for o in (out, other):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            B.prompt_attention(q, k, v, cq, cu_seqlens_k=ck, out=o, status=st)
+    for n, m in ((40, 5000), (40, 6000), (3, 2000), (40, 50), (40, 5000)):
+        cq.copy_(cu([n]))
+        ck.copy_(cu([m]))
+        for o in (out, other):
+            o.zero_()
+        for g in (*graphs, graphs[0]):
+            g.replay()
+        torch.cuda.synchronize()
+        want = B.prompt_attention(q, k, v, cq, cu_seqlens_k=ck)[0]
+        for o in (out, other):
+            assert torch.equal(o[:n], want[:n]) and not o[n:].any()
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("batch", [385, 3000])
+def test_a_large_batch_of_short_prompts(B, batch):
+    # Lengths 0 to 4, here and there 70: every sequence by itself is the same sequence.
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 5, (batch,), generator=g)
+    lens[::97] = 70
+    n = int(lens.sum())
+    q, k, v = draw(1, n, 8, 64), draw(2, n, 4, 64), draw(3, n, 4, 64)
+    out, lse, st = B.prompt_attention(q, k, v, cu(lens.tolist()), return_lse=True)
+    assert int(st.item()) == 0
+    at = [0, *lens.cumsum(0).tolist()]
+    for r in (0, 1, 2, 96, 97, 98, 383, 384, batch - 2, batch - 1):
+        a, b = at[r], at[r + 1]
+        one, one_lse, _ = B.prompt_attention(q[a:b], k[a:b], v[a:b], cu([b - a]), return_lse=True)
+        assert torch.equal(out[a:b], one) and torch.equal(lse[a:b], one_lse), r
+    # every row is written: the whole against one call per hundred sequences
+    for r in range(0, batch, 100):
+        a, b = at[r], at[min(r + 100, batch)]
+        part, _, _ = B.prompt_attention(q[a:b], k[a:b], v[a:b], cu(lens[r:r + 100].tolist()))
+        assert torch.equal(out[a:b], part), r
+
+
+def test_lengths_that_overlap_leave_no_row_out(B):
+    # The descending boundaries are flagged; the three sequences between them are the same rows.
+    q, k, v = draw(1, 512, 2, 64), draw(2, 512, 1, 64), draw(3, 512, 1, 64)
+    want = B.prompt_attention(q, k, v, cu([512]))[0]
+    bad = torch.tensor([0, 512, 0, 512, 0, 512], dtype=torch.int32, device="cuda")
+    out, _, st = B.prompt_attention(q, k, v, bad)
+    assert int(st.item()) == B.DEV_STATUS["bad_seqlen"] and torch.equal(out, want)
+
+
 def test_refusals(B):
     q, k, v, c = draw(1, 8, 8, 64), draw(2, 8, 2, 64), draw(3, 8, 2, 64), cu([8])
     for args, kw, what in (((q.float(), k, v, c), {}, "dtype"), ((q, k, v[:4], c), {}, "agree"),
