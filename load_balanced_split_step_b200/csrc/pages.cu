@@ -16,7 +16,12 @@
 //
 // The data is moved by pages_copy_kernel, for any number of caches (the K and V of every layer
 // share the table), from the list a planner leaves on the device. A destination was free and a
-// source is live, so no page is both.
+// source is live, so no page is both. 16 bytes a thread, four loads in flight, 8 CTAs of 256 threads per SM: 268 MB in
+// 98 us with a planner ahead (5.5 TB/s of reads and writes).
+//
+// The planners are bound by latency, about ten dependent accesses and four barriers: a fork of a batch of beams
+// with its copy takes 8 us, a resize of 256 requests in a pool of 40000 pages with its copy 15 us (16.3 before the new
+// table was written under the first phases).
 #include "hpc_common.cuh"
 
 namespace hpc {

@@ -17,6 +17,9 @@ definitions by eye:
   unit, and the static split-k plan it replaces.
 * ``merge``: per-split softmax states and their log-sum-exp merge.
 * ``prologue``: RMSNorm, NeoX RoPE and the KV-page write of the new token.
+* ``prompt``: attention of one prompt, causal or not, with its log-sum-exp.
+* ``verify``: which drafted tokens stand, and the token after them.
+* ``pages``: resize, fork and compact of a paged cache by reference counts.
 * ``fp8``: OCP E4M3 decode and encode (round to nearest even, saturating).
 
 Pins (tests/test_oracle_*.py) tie each function to something other than itself:
