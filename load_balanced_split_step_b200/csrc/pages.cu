@@ -19,9 +19,11 @@
 // source is live, so no page is both. 16 bytes a thread, four loads in flight, 8 CTAs of 256 threads per SM: 268 MB in
 // 98 us with a planner ahead (5.5 TB/s of reads and writes).
 //
-// The planners are bound by latency, about ten dependent accesses and four barriers: a fork of a batch of beams
-// with its copy takes 8 us, a resize of 256 requests in a pool of 40000 pages with its copy 15 us (16.3 before the new
-// table was written under the first phases).
+// The planners are bound by latency (about eight dependent accesses and three to four barriers) and, in large pools, by
+// what eight SMs copy: a resize of 256 requests in a pool of 40000 pages takes 11.5 us, of 4 requests in one of 512
+// 5.7 us; forks 13.7 and 7.2 us. Each warp reads its run of counts once and keeps it as bits; lengths and
+// entries that later phases want are loaded under the copy of the counts; divisions are 32-bit (12.9 and 6.6 us without
+// the three).
 #include "hpc_common.cuh"
 
 namespace hpc {
@@ -31,6 +33,7 @@ constexpr int kPgCtas = 8;        // one portable cluster
 constexpr int kPgThreads = 1024;  // per CTA
 constexpr int kPgWarps = kPgThreads / 32;
 constexpr int kPgAllWarps = kPgCtas * kPgWarps;
+constexpr int kPgHeld = 8;
 constexpr int kPgMaxRows = 8192;  // rows whose needs fit in shared memory (12 bytes each at most)
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -65,30 +68,42 @@ __device__ __forceinline__ int2 ld_shared_state(const int2* p) {
 }
 
 
-// In place, s[0 .. n) -> exclusive prefix sums, returns the total (whole block).
-__device__ int32_t block_prefix(int32_t* s, int32_t n, int32_t* s_red) {
+// In place, the kN arrays s[k][0 .. n) -> exclusive prefix sums; their totals (whole block).
+template <int kN>
+__device__ __forceinline__ void block_prefix(int32_t* const (&s)[kN], int32_t n, int32_t (&red)[2][kPgWarps],
+                                             int32_t (&total)[kN]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t base = 0;
-  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kN; ++k) total[k] = 0;
   for (int32_t i0 = 0; i0 < n; i0 += kPgThreads) {
     const int32_t i = i0 + static_cast<int32_t>(threadIdx.x);
-    const int32_t v = i < n ? s[i] : 0;
-    int32_t x = v;
+    int32_t v[kN], x[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) x[k] = v[k] = i < n ? s[k][i] : 0;  // the thread's own entry
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+        if (lane >= o) x[k] += y;
+      }
+    }
+    if (i0 > 0) __syncthreads();  // the sums before are read
+    if (lane == 31) {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) red[k][warp] = x[k];
     }
     __syncthreads();
-    if (lane == 31) s_red[warp] = x;
-    __syncthreads();
-    const int32_t w = s_red[lane];
-    const int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
-    if (i < n) s[i] = base + before + x - v;
-    base += __reduce_add_sync(0xffffffffu, w);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int32_t w = red[k][lane];
+      if (i < n) s[k][i] = total[k] + x[k] - v[k];
+      const int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+      if (i < n) s[k][i] += before;
+      total[k] += __reduce_add_sync(0xffffffffu, w);
+    }
   }
   __syncthreads();
-  return base;
 }
 
 // Largest i with s[i] <= k, for an ascending prefix s[0 .. n) with s[0] = 0.
@@ -103,9 +118,9 @@ __device__ __forceinline__ int32_t prefix_find(const int32_t* s, int32_t n, int3
 }
 
 struct PgShared {
-  int32_t red[kPgWarps];
-  int32_t a[kPgCtas], b[kPgCtas];  // per CTA of the cluster
-  int32_t wa[kPgWarps], wb[kPgWarps];
+  int32_t red[2][kPgWarps];
+  int32_t a[kPgCtas];  // per CTA of the cluster
+  int32_t wa[kPgWarps];
 };
 
 // The run of pages [begin, end) of a warp: the pool in 256 contiguous runs.
@@ -116,31 +131,62 @@ __device__ __forceinline__ void warp_run(int32_t num_pages, int32_t gw, int32_t&
   end = static_cast<int32_t>(e < num_pages ? e : num_pages);
 }
 
-// Count of the pages of [begin, end) that `want` holds for (whole warp).
-template <typename F>
-__device__ __forceinline__ int32_t warp_count(const int32_t* ref, int32_t begin, int32_t end, F want) {
-  const int lane = threadIdx.x & 31;
-  int32_t c = 0;
-#pragma unroll 4
-  for (int32_t p = begin + lane; p < end; p += 32) c += want(p, ld_shared_state(ref + p)) ? 1 : 0;
-  return __reduce_add_sync(0xffffffffu, c);
+__device__ __forceinline__ uint32_t low_bits(int32_t n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+
+// Which of the 32 pages from p0 on are in use (whole warp; none at or past the end of the run).
+__device__ __forceinline__ uint32_t used_pages(const int32_t* ref, int32_t p0, int32_t end) {
+  const int32_t p = p0 + (threadIdx.x & 31);
+  return __ballot_sync(0xffffffffu, p < end && ld_shared_state(ref + p) != 0);
 }
 
-// Calls visit(page, rank) for the pages of [begin, end) that `want` holds for, ranks ascending from
-// `rank`, until `limit` (whole warp).
-template <typename F, typename V>
-__device__ __forceinline__ void warp_visit(const int32_t* ref, int32_t begin, int32_t end, int32_t rank, int32_t limit,
-                                           F want, V visit) {
-  const int lane = threadIdx.x & 31;
-  for (int32_t p0 = begin; p0 < end && rank < limit; p0 += 32) {
-    const int32_t p = p0 + lane;
-    const bool w = p < end && want(p, ld_shared_state(ref + p));
-    const uint32_t m = __ballot_sync(0xffffffffu, w);
-    const int32_t k = rank + __popc(m & ((1u << lane) - 1u));
-    if (w && k < limit) visit(p, k);
-    rank += __popc(m);
+// A warp's run of pages as bits, read once for counting and for handing out: kPgHeld groups of 32 in registers (all
+// of a pool of 65536), the rest from memory again. `pick` turns the bits of a group into those that are asked for.
+struct PgRun {
+  const int32_t* ref;
+  int32_t begin, end;
+  uint32_t used[kPgHeld];
+
+  __device__ __forceinline__ PgRun(const int32_t* r, int32_t num_pages, int32_t gw) : ref(r) {
+    warp_run(num_pages, gw, begin, end);
+    int32_t c[kPgHeld];
+#pragma unroll
+    for (int g = 0; g < kPgHeld; ++g) {
+      const int32_t p = begin + 32 * g + static_cast<int32_t>(threadIdx.x & 31);
+      c[g] = p < end ? ld_shared_state(ref + p) : 0;
+    }
+#pragma unroll
+    for (int g = 0; g < kPgHeld; ++g) used[g] = __ballot_sync(0xffffffffu, c[g] != 0);
   }
-}
+  __device__ __forceinline__ uint32_t valid(int32_t p0) const { return low_bits(end - p0); }
+
+  template <typename F>
+  __device__ __forceinline__ int32_t count(F pick) const {
+    int32_t n = 0;
+#pragma unroll
+    for (int g = 0; g < kPgHeld; ++g) n += __popc(pick(used[g], begin + 32 * g));
+    for (int32_t p0 = begin + 32 * kPgHeld; p0 < end; p0 += 32) n += __popc(pick(used_pages(ref, p0, end), p0));
+    return n;
+  }
+  // visit(page, rank) for the pages that are picked, ranks ascending from `rank`, until `limit`.
+  template <typename F, typename V>
+  __device__ __forceinline__ void visit(int32_t rank, int32_t limit, F pick, V visit) const {
+    const int lane = threadIdx.x & 31;
+    auto group = [&](uint32_t m, int32_t p0) {
+      const int32_t k = rank + __popc(m & ((1u << lane) - 1u));
+      if ((m >> lane & 1u) && k < limit) visit(p0 + lane, k);
+      rank += __popc(m);
+    };
+#pragma unroll 1
+    for (int g = 0; g < kPgHeld && rank < limit; ++g) {
+      uint32_t m = used[0];
+#pragma unroll
+      for (int i = 1; i < kPgHeld; ++i) m = g == i ? used[i] : m;
+      if (begin + 32 * g < end) group(pick(m, begin + 32 * g), begin + 32 * g);
+    }
+    for (int32_t p0 = begin + 32 * kPgHeld; p0 < end && rank < limit; p0 += 32)
+      group(pick(used_pages(ref, p0, end), p0), p0);
+  }
+};
 
 // Per-warp counts -> this warp's exclusive prefix over the cluster and the total. Every thread of
 // the cluster calls it, after a first cluster_sync (a CTA's shared memory may be written only once it
@@ -187,15 +233,18 @@ struct PgArgs {
   int2* moves;              // (source page, destination page)
   int32_t* n_moves;
   uint32_t* status;
-  int32_t rows_in, rows_out, max_pages, num_pages, page_size;
+  int32_t rows_in, rows_out, max_pages, num_pages, page_size, max_len;
 };
 
-__device__ __forceinline__ bool len_ok(const PgArgs& a, int64_t n) {
-  return n >= 0 && n <= static_cast<int64_t>(a.max_pages) * a.page_size;
+// Lengths and page_size fit in 31 bits together (max_len = max_pages * page_size): 32-bit divisions.
+__device__ __forceinline__ bool len_ok(const PgArgs& a, int32_t n) { return n >= 0 && n <= a.max_len; }
+__device__ __forceinline__ int32_t held(const PgArgs& a, int32_t n) {
+  return static_cast<int32_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(a.page_size) - 1u) / static_cast<uint32_t>(a.page_size));
 }
-__device__ __forceinline__ int32_t held(const PgArgs& a, int64_t n) {
-  return static_cast<int32_t>((n + a.page_size - 1) / a.page_size);
+__device__ __forceinline__ int32_t column(const PgArgs& a, int32_t n) {  // of token n
+  return static_cast<int32_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(a.page_size));
 }
+__device__ __forceinline__ bool part_filled(const PgArgs& a, int32_t n) { return column(a, n) * a.page_size != n; }
 
 // ---- resize -----------------------------------------------------------------------------
 // Row r goes from lens[r] to want[r] tokens. Pages past the new length are released (count - 1); a row
@@ -210,41 +259,58 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   const uint32_t rank = cluster_rank();
   const int32_t gtid = static_cast<int32_t>(rank) * kPgThreads + static_cast<int32_t>(threadIdx.x);
   const int32_t gw = gtid >> 5;
-  const int32_t M = a.max_pages, P = a.page_size, rows = a.rows_out;
+  const int32_t M = a.max_pages, rows = a.rows_out;
   pdl_wait();
   pdl_launch_dependents();
+
+  // Lengths and entries that later phases want, of this warp's and this thread's first rows: loaded under the copy.
+  const int32_t t = static_cast<int32_t>(threadIdx.x);
+  const int32_t row_old = gw < rows ? a.lens[gw] : 0, row_new = gw < rows ? a.want[gw] : 0;
+  const int32_t own_old = t < rows ? a.lens[t] : 0, own_new = t < rows ? a.want[t] : 0;
+  auto lengths = [&](int32_t r, int32_t& o, int32_t& n) {  // of a row of the warp
+    o = r == gw ? row_old : a.lens[r];
+    n = r == gw ? row_new : a.want[r];
+    return len_ok(a, o) && len_ok(a, n);
+  };
+  copy_counts(a.ref_in, a.ref_out, a.num_pages, gtid);
+  // the first 32 entries that the warp's first row releases
+  const bool row_shrinks = gw < rows && len_ok(a, row_old) && len_ok(a, row_new) && row_new < row_old;
+  const int32_t row_from = row_shrinks ? held(a, row_new) + lane : 0;
+  const int32_t row_entry = row_shrinks && row_from < held(a, row_old) ? a.table_in[static_cast<int64_t>(gw) * M + row_from] : 0;
+  // the part-filled page that the thread's first row grows in
+  const bool own_grows = t < rows && len_ok(a, own_old) && len_ok(a, own_new) && own_new > own_old;
+  const int32_t own_page = own_grows && part_filled(a, own_old) ? a.table_in[static_cast<int64_t>(t) * M + column(a, own_old)] : 0;
 
   // The entries that stay, and -1 past them; the new ones are written below by whoever holds the page. A new
   // table is written now, under the latencies of the first phases, and an old one once nothing can fail.
   auto keep_entries = [&]() {
     for (int32_t r = gw; r < rows; r += kPgAllWarps) {
-      const int64_t o = a.lens[r], n = a.want[r];
-      const bool ok = len_ok(a, o) && len_ok(a, n);
+      int32_t o, n;
+      const bool ok = lengths(r, o, n);
       const int32_t from = ok ? held(a, o) : M, to = ok ? held(a, n) : M;
       const int32_t keep = from < to ? from : to;
       const int32_t* in = a.table_in + static_cast<int64_t>(r) * M;
       int32_t* out = a.table_out + static_cast<int64_t>(r) * M;
       if (in != out) {
-#pragma unroll 4
+#pragma unroll 8
         for (int32_t j = lane; j < keep; j += 32) out[j] = in[j];
       }
 #pragma unroll 4
       for (int32_t j = to + lane; j < M; j += 32) out[j] = -1;
     }
   };
-  copy_counts(a.ref_in, a.ref_out, a.num_pages, gtid);
   if (a.table_in != a.table_out) keep_entries();
   cluster_sync();
   // releases; `sign` +1 takes them back
   auto release = [&](int32_t sign) {
     for (int32_t r = gw; r < rows; r += kPgAllWarps) {
-      const int64_t o = a.lens[r], n = a.want[r];
-      if (!len_ok(a, o) || !len_ok(a, n)) {
+      int32_t o, n;
+      if (!lengths(r, o, n)) {
         if (lane == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
         continue;
       }
       for (int32_t j = held(a, n) + lane; j < held(a, o); j += 32) {
-        const int32_t p = a.table_in[static_cast<int64_t>(r) * M + j];
+        const int32_t p = r == gw && j == row_from ? row_entry : a.table_in[static_cast<int64_t>(r) * M + j];
         if (p >= 0 && p < a.num_pages) atomicAdd(a.ref_out + p, sign);
         else atomicOr(a.status, HPC_DEV_BAD_PAGE);
       }
@@ -252,14 +318,15 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   };
   release(-1);
   cluster_sync();
+  const PgRun run(a.ref_out, a.num_pages, gw);
   // what every row needs, in every CTA
-  for (int32_t r = threadIdx.x; r < rows; r += kPgThreads) {
-    const int64_t o = a.lens[r], n = a.want[r];
+  for (int32_t r = t; r < rows; r += kPgThreads) {
+    const int32_t o = r == t ? own_old : a.lens[r], n = r == t ? own_new : a.want[r];
     int32_t need = 0, cow = 0;
     if (len_ok(a, o) && len_ok(a, n) && n > o) {
       need = held(a, n) - held(a, o);
-      if (o % P != 0) {
-        const int32_t p = a.table_in[static_cast<int64_t>(r) * M + o / P];
+      if (part_filled(a, o)) {
+        const int32_t p = r == t ? own_page : a.table_in[static_cast<int64_t>(r) * M + column(a, o)];
         if (p < 0 || p >= a.num_pages) atomicOr(a.status, HPC_DEV_BAD_PAGE);
         else if (ld_shared_state(a.ref_out + p) > 1) cow = 1;
       }
@@ -267,12 +334,12 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     s_need[r] = need + cow;
     s_cow[r] = cow;
   }
-  const int32_t total = block_prefix(s_need, rows, sh.red);
-  const int32_t copies = block_prefix(s_cow, rows, sh.red);
-  int32_t begin, end, before, free_pages;
-  warp_run(a.num_pages, gw, begin, end);
-  auto is_free = [](int32_t, int32_t c) { return c == 0; };
-  cluster_prefix(warp_count(a.ref_out, begin, end, is_free), sh.a, sh.wa, before, free_pages);
+  int32_t totals[2];
+  block_prefix<2>({s_need, s_cow}, rows, sh.red, totals);
+  const int32_t total = totals[0], copies = totals[1];
+  int32_t before, free_pages;
+  auto is_free = [&](uint32_t used, int32_t p0) { return ~used & run.valid(p0); };
+  cluster_prefix(run.count(is_free), sh.a, sh.wa, before, free_pages);
   const bool fits = total <= free_pages;
   if (gtid == 0) *a.n_moves = fits ? copies : 0;
   if (!fits) {
@@ -284,13 +351,13 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     return;
   }
   if (a.table_in == a.table_out) keep_entries();
-  warp_visit(a.ref_out, begin, end, before, total, is_free, [&](int32_t p, int32_t k) {
+  run.visit(before, total, is_free, [&](int32_t p, int32_t k) {
     const int32_t r = prefix_find(s_need, rows, k);
-    const int64_t o = a.lens[r];
+    const int32_t o = a.lens[r];
     const bool cow = (r + 1 < rows ? s_cow[r + 1] : copies) != s_cow[r];
     const int32_t nth = k - s_need[r];
     const bool copy = cow && nth == 0;
-    const int32_t j = copy ? static_cast<int32_t>(o / P) : held(a, o) + nth - (cow ? 1 : 0);
+    const int32_t j = copy ? column(a, o) : held(a, o) + nth - (cow ? 1 : 0);
     const int64_t i = static_cast<int64_t>(r) * M + j;
     if (copy) a.moves[s_cow[r]] = make_int2(a.table_in[i], p);  // the entry itself is this thread's
     a.table_out[i] = p;
@@ -321,18 +388,24 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   const uint32_t rank = cluster_rank();
   const int32_t gtid = static_cast<int32_t>(rank) * kPgThreads + static_cast<int32_t>(threadIdx.x);
   const int32_t gw = gtid >> 5;
-  const int32_t M = a.max_pages, P = a.page_size, rows = a.rows_out;
+  const int32_t M = a.max_pages, rows = a.rows_out;
   pdl_wait();
   pdl_launch_dependents();
 
+  // Parents and lengths of this thread's and this warp's first rows: loaded under the copy.
+  const int32_t t = static_cast<int32_t>(threadIdx.x);
+  const int32_t own_f = t < rows ? a.want[t] : -1, row_f = gw < rows ? a.want[gw] : -1;
+  const int32_t src_len = gw < a.rows_in ? a.lens[gw] : 0;
   copy_counts(a.ref_in, a.ref_out, a.num_pages, gtid);
+  const int32_t own_len = own_f >= 0 && own_f < a.rows_in ? a.lens[own_f] : 0;
+  const int32_t row_len = row_f >= 0 && row_f < a.rows_in ? a.lens[row_f] : 0;
   for (int32_t s = threadIdx.x; s < a.rows_in; s += kPgThreads) {
     s_kids[s] = 0;
     s_first[s] = rows;
   }
   __syncthreads();
   for (int32_t r = threadIdx.x; r < rows; r += kPgThreads) {
-    const int32_t f = a.want[r];
+    const int32_t f = r == t ? own_f : a.want[r];
     if (f >= 0 && f < a.rows_in) {
       atomicAdd(s_kids + f, 1);
       atomicMin(s_first + f, r);
@@ -342,29 +415,31 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   }
   __syncthreads();
   // length of new row r (0 for an empty row or a parent with an invalid length)
-  auto length = [&](int32_t r, int32_t& f) -> int64_t {
+  auto length = [&](int32_t r, int32_t& f) -> int32_t {
     f = a.want[r];
     if (f < 0 || f >= a.rows_in) return 0;
-    const int64_t n = a.lens[f];
+    const int32_t n = a.lens[f];
     return len_ok(a, n) ? n : 0;
   };
   for (int32_t r = threadIdx.x; r < rows; r += kPgThreads) {
-    int32_t f;
-    const int64_t n = length(r, f);
-    s_need[r] = n % P != 0 && s_first[f] != r ? 1 : 0;
+    int32_t f = own_f;
+    const int32_t n = r == t ? (len_ok(a, own_len) ? own_len : 0) : length(r, f);
+    s_need[r] = part_filled(a, n) && s_first[f] != r ? 1 : 0;
   }
-  const int32_t total = block_prefix(s_need, rows, sh.red);
+  int32_t totals[1];
+  block_prefix<1>({s_need}, rows, sh.red, totals);
+  const int32_t total = totals[0];
   // The rows, but for the pages that are copied: those are written below by whoever holds the new page.
   auto write_rows = [&](bool filled) {
     for (int32_t r = gw; r < rows; r += kPgAllWarps) {
-      int32_t f = 0;
-      const int64_t n = filled ? length(r, f) : 0;
-      if (lane == 0) a.lens_out[r] = static_cast<int32_t>(n);
+      int32_t f = row_f;
+      const int32_t n = !filled ? 0 : (r == gw ? (len_ok(a, row_len) ? row_len : 0) : length(r, f));
+      if (lane == 0) a.lens_out[r] = n;
       const int32_t np = held(a, n);
       const bool fresh = (r + 1 < rows ? s_need[r + 1] : total) != s_need[r];
       const int32_t* in = a.table_in + static_cast<int64_t>(f < 0 ? 0 : f) * M;
       int32_t* out = a.table_out + static_cast<int64_t>(r) * M;
-#pragma unroll 4
+#pragma unroll 8
       for (int32_t j = lane; j < np - (fresh ? 1 : 0); j += 32) out[j] = in[j];
 #pragma unroll 4
       for (int32_t j = np + lane; j < M; j += 32) out[j] = -1;
@@ -376,7 +451,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   // page one child keeps the reference and the others leave.
   auto recount = [&](int32_t sign) {
     for (int32_t s = gw; s < a.rows_in; s += kPgAllWarps) {
-      const int64_t n = a.lens[s];
+      const int32_t n = s == gw ? src_len : a.lens[s];
       if (!len_ok(a, n)) {
         if (lane == 0) atomicOr(a.status, HPC_DEV_BAD_SEQLEN);
         continue;
@@ -384,7 +459,7 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
       const int32_t kids = s_kids[s], np = held(a, n);
       for (int32_t j = lane; j < np; j += 32) {
         const int32_t p = a.table_in[static_cast<int64_t>(s) * M + j];
-        const bool part = j == np - 1 && n % P != 0;
+        const bool part = j == np - 1 && part_filled(a, n);
         const int32_t d = part ? (kids > 0 ? 0 : -1) : kids - 1;
         if (p < 0 || p >= a.num_pages) atomicOr(a.status, HPC_DEV_BAD_PAGE);
         else if (d != 0) atomicAdd(a.ref_out + p, sign * d);
@@ -393,10 +468,10 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   };
   recount(1);
   cluster_sync();
-  int32_t begin, end, before, free_pages;
-  warp_run(a.num_pages, gw, begin, end);
-  auto is_free = [](int32_t, int32_t c) { return c == 0; };
-  cluster_prefix(warp_count(a.ref_out, begin, end, is_free), sh.a, sh.wa, before, free_pages);
+  const PgRun run(a.ref_out, a.num_pages, gw);
+  int32_t before, free_pages;
+  auto is_free = [&](uint32_t used, int32_t p0) { return ~used & run.valid(p0); };
+  cluster_prefix(run.count(is_free), sh.a, sh.wa, before, free_pages);
   const bool fits = total <= free_pages;
   if (gtid == 0) {
     *a.n_moves = fits ? total : 0;
@@ -407,11 +482,11 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
     write_rows(false);
     return;
   }
-  warp_visit(a.ref_out, begin, end, before, total, is_free, [&](int32_t p, int32_t k) {
+  run.visit(before, total, is_free, [&](int32_t p, int32_t k) {
     const int32_t r = prefix_find(s_need, rows, k);
     int32_t f;
-    const int64_t n = length(r, f);
-    const int32_t j = static_cast<int32_t>(n / P);
+    const int32_t n = length(r, f);
+    const int32_t j = column(a, n);
     a.moves[k] = make_int2(a.table_in[static_cast<int64_t>(f) * M + j], p);
     a.table_out[static_cast<int64_t>(r) * M + j] = p;
     a.ref_out[p] = 1;
@@ -428,18 +503,19 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
   const int32_t gw = gtid >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  int32_t begin, end, unused, n, src0, srcs, dst0, dsts;
-  warp_run(a.num_pages, gw, begin, end);
+  int32_t used_before, n, src0, srcs;
+  const PgRun run(a.ref_in, a.num_pages, gw);
   cluster_sync();
-  cluster_prefix(warp_count(a.ref_in, begin, end, [](int32_t, int32_t c) { return c != 0; }), s_c, s_w, unused, n);
-  auto is_src = [n](int32_t p, int32_t c) { return c != 0 && p >= n; };
-  auto is_dst = [n](int32_t p, int32_t c) { return c == 0 && p < n; };
-  cluster_prefix(warp_count(a.ref_in, begin, end, is_src), sh.a, sh.wa, src0, srcs);
-  cluster_prefix(warp_count(a.ref_in, begin, end, is_dst), sh.b, sh.wb, dst0, dsts);
-  // srcs == dsts: the used pages below n and the sources make up n
-  warp_visit(a.ref_in, begin, end, src0, srcs, is_src, [&](int32_t p, int32_t k) { a.moves[k].x = p; });
-  warp_visit(a.ref_in, begin, end, dst0, dsts, is_dst, [&](int32_t p, int32_t k) { a.moves[k].y = p; });
-  for (int32_t p = begin + (threadIdx.x & 31); p < end; p += 32) {
+  cluster_prefix(run.count([](uint32_t used, int32_t) { return used; }), s_c, s_w, used_before, n);
+  auto is_src = [&](uint32_t used, int32_t p0) { return used & ~low_bits(n - p0); };
+  auto is_dst = [&](uint32_t used, int32_t p0) { return ~used & low_bits(n - p0) & run.valid(p0); };
+  cluster_prefix(run.count(is_src), sh.a, sh.wa, src0, srcs);
+  // There are as many destinations: the used pages below n and the sources make up n. A run that has some starts
+  // below n, behind begin - used_before free pages.
+  run.visit(src0, srcs, is_src, [&](int32_t p, int32_t k) { a.moves[k].x = p; });
+  run.visit(run.begin - used_before, srcs, is_dst, [&](int32_t p, int32_t k) { a.moves[k].y = p; });
+#pragma unroll 4
+  for (int32_t p = run.begin + (threadIdx.x & 31); p < run.end; p += 32) {
     const int32_t c = a.ref_in[p];
     if (a.ref_in != a.ref_out) a.ref_out[p] = c;
     a.page_map[p] = c != 0 ? p : -1;
@@ -564,6 +640,7 @@ extern "C" int hpc_pages_resize(const int32_t* table_in, int32_t* table_out, int
   a.max_pages = max_pages_per_req;
   a.num_pages = num_pages;
   a.page_size = page_size;
+  a.max_len = max_pages_per_req * page_size;
   return launch_planner(pages_resize_kernel, "pages_resize_kernel", a, static_cast<size_t>(batch) * 8, stream);
 }
 
@@ -595,6 +672,7 @@ extern "C" int hpc_pages_fork(const int32_t* table_in, const int32_t* lens_in, i
   a.max_pages = max_pages_per_req;
   a.num_pages = num_pages;
   a.page_size = page_size;
+  a.max_len = max_pages_per_req * page_size;
   return launch_planner(pages_fork_kernel, "pages_fork_kernel", a,
                         (static_cast<size_t>(rows_out) + 2 * static_cast<size_t>(rows_in)) * 4, stream);
 }
