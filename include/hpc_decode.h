@@ -541,7 +541,8 @@ HPC_API int hpc_prompt_attention(const void* q, int64_t q_token_stride, int64_t 
 
 /* hpc_prompt_attention, causal, with the keys and values of request r in the pages of the cache: its
  * seq_lens[r] cached tokens, the last cu_seqlens[r+1] - cu_seqlens[r] of which are the queries (a chunk of a
- * prompt, or a prompt behind a cached prefix). BF16 caches, page_size 16, 32, 64 or 128; block_table and
+ * prompt, or a prompt behind a cached prefix). BF16 caches, page_size 16, 32, 64 or 128 (hpc_gather_tokens and
+ * hpc_prompt_attention serve the others); block_table and
  * seq_lens as hpc_decode_attention. seq_lens[r] below the number of queries or beyond the block table sets
  * HPC_DEV_BAD_SEQLEN and leaves the request out; a page id out of range sets HPC_DEV_BAD_PAGE, and the
  * request's output is unspecified. */
@@ -553,6 +554,22 @@ HPC_API int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride, in
                                        int32_t kv_heads, int32_t head_dim, float sm_scale, void* out, float* lse,
                                        uint32_t* work, void* partial, size_t partial_bytes, uint32_t* status,
                                        void* stream);
+
+/* The cached tokens of every request as packed bf16 rows, for what reads packed keys: prompt attention over an
+ * E4M3 cache or over pages of a size of its own (hpc_prompt_attention with cu_seqlens as cu_seqlens_k).
+ *   k_out, v_out: device bf16 [kv_tokens][kv_heads][head_dim], 16-byte aligned: request r's tokens are rows
+ *               [cu_seqlens[r], cu_seqlens[r+1]), E4M3 values times their scale, rounded to bf16. Rows past
+ *               cu_seqlens[batch] are left as they were.
+ *   cu_seqlens: device int32 [batch + 1], written: the prefix sums of the lengths.
+ *   Caches, scales, block_table, seq_lens as hpc_decode_prologue; any page_size; batch <= 8192.
+ * Requests from the first on that does not fit into kv_tokens rows are left out (no rows) and set
+ * HPC_DEV_CAPACITY. A length that is negative or beyond the block table counts as 0 and sets
+ * HPC_DEV_BAD_SEQLEN; tokens of a page out of range are zeros and set HPC_DEV_BAD_PAGE. */
+HPC_API int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype, hpc_kv_layout kv_layout,
+                              const float* k_scale, const float* v_scale, int32_t num_pages, int32_t page_size,
+                              const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
+                              int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t kv_tokens, void* k_out,
+                              void* v_out, int32_t* cu_seqlens, uint32_t* status, void* stream);
 
 /* ---- verification of drafted tokens -----------------------------------------------------
  * After hpc_decode_step_multi has run the target over the drafted tokens: which of them stand, and the

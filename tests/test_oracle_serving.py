@@ -189,3 +189,19 @@ def test_host_checks_of_prompt_attention(B):
     assert paged(P=8) == paged(P=48) == paged(P=256) == paged(M=1 << 28) == B.HPC_ERR_SHAPE
     assert paged(k=odd) == B.HPC_ERR_ALIGN and paged() == B.HPC_OK
     assert lib.hpc_prompt_attention_partial_bytes(96) == 0 and lib.hpc_prompt_attention_partial_bytes(64) > 0
+
+
+def test_host_checks_of_gather_tokens(B):
+    w, odd = ctypes.c_void_p(256), ctypes.c_void_p(264)
+    lib = B._lib
+
+    def gather(k=w, kv=B.HPC_BF16, lay=B.HPC_HND, ks=None, N=4, P=16, table=w, M=3, lens=w, batch=2, H=2, D=128, n=8, ko=w,
+               cu=w):
+        return lib.hpc_gather_tokens(k, w, kv, lay, ks, ks, N, P, table, M, lens, batch, H, D, n, ko, w, cu, w, None)
+
+    for bad in (dict(k=None), dict(table=None), dict(lens=None), dict(cu=None), dict(ko=None), dict(lay=2), dict(N=0),
+                dict(P=0), dict(M=0), dict(batch=0), dict(H=0), dict(n=-1), dict(n=1 << 31), dict(kv=B.HPC_E4M3)):
+        assert gather(**bad) == B.HPC_ERR_ARG, bad
+    assert gather(kv=B.HPC_FP32) == B.HPC_ERR_DTYPE
+    assert gather(D=96) == gather(batch=8193) == gather(H=65537) == B.HPC_ERR_SHAPE
+    assert gather(k=odd) == gather(ko=odd) == B.HPC_ERR_ALIGN
