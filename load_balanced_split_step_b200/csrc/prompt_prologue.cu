@@ -10,14 +10,15 @@
 // wide, the rotation needs no exchange, and the mean square is reduced over D/16 lanes. A warp
 // therefore takes 512/D heads of one token at a time, two such groups in work and the next two on their way. It
 // computes its token's D/2 angles itself (one or two per lane) and never meets another warp; norm weights and
-// rotation are folded into four factors per pair, once per token. Where there are few tokens, the heads of one are split over
-// several warps, which each repeat the angles: up to about 8 warps per SM, latency is what counts.
+// rotation are folded into four factors per pair, once per token, and applied two floats at a time. Warps take equal
+// runs of groups, parts of tokens too (whole tokens left a seventh of the warps idle at 8192 tokens).
 //
-// 8192 tokens of 64/8 heads of 128 into an E4M3 cache: 76 us, 4.4 TB/s of reads and writes (85 us before the factors were
-// folded and the next heads loaded ahead). 100 tokens of 8/2 heads of 64: 4.6 us with the launch.
+// 8192 tokens of 64/8 heads of 128 into an E4M3 cache: 61 us, 5.5 TB/s of reads and writes (76 us with whole tokens, single
+// floats and a division per element); 5 or 6 CTAs per SM spill and take 73 and 81. 100 tokens of 8/2 heads of 64: 3.0 us.
 #include <cmath>
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "hpc_common.cuh"
 
 namespace hpc {
@@ -44,7 +45,7 @@ struct PpArgs {
   int64_t tokens, max_pages;
   double log2_theta;
   float eps;
-  int32_t batch, Hq, Hkv, num_pages, P, nhd, fp8, parts;
+  int32_t batch, Hq, Hkv, num_pages, P, nhd, fp8;
 };
 
 // The request that token i belongs to: the last r with cu[r] <= i (whole warp, 32 probes a step).
@@ -64,23 +65,38 @@ __device__ __forceinline__ int32_t find_request(const int32_t* cu, int32_t batch
   return lo;
 }
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+// 8 elements as 4 pairs.
+__device__ __forceinline__ void unpack8(uint4 v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                    pack_bf16x2(f[3].x, f[3].y));
+}
+
+// x / sc as E4M3, by the reciprocal and one step of the remainder (Markstein's correction: q + r (x - q sc), which
+// leaves the rounded quotient but for rare last bits, far below an E4M3 step): a division for every element took 5 of 65
+// us. The bound keeps a quotient that overflows from turning into NaN; it saturates.
+__device__ __forceinline__ uint2 pack8_e4m3(const float2 (&f)[4], float sc) {
+  const float r = 1.f / sc, top = 1.2676506e30f;  // 2^100
+  const float2 r2 = make_float2(r, r), sc2 = make_float2(-sc, -sc);
+  float2 q[4];
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    float2 p = mul2(f[k], r2);
+    p = make_float2(fminf(fmaxf(p.x, -top), top), fminf(fmaxf(p.y, -top), top));
+    q[k] = fma2(fma2(p, sc2, f[k]), r2, p);
+    q[k] = make_float2(copysignf(q[k].x, p.x), copysignf(q[k].y, p.y));  // -0 stays one
   }
+  return make_uint2(f32x4_to_e4m3x4(q[0].x, q[0].y, q[1].x, q[1].y), f32x4_to_e4m3x4(q[2].x, q[2].y, q[3].x, q[3].y));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+__device__ __forceinline__ void load8(const float* p, float2 (&f)[4]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
 
 template <int D>
@@ -105,18 +121,22 @@ __global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(co
   }
   __syncthreads();
   const int32_t first = a.cu[0], past = a.cu[a.batch];
-  // Each warp takes consecutive units, so that a request is looked up once for a run of its tokens.
-  const int64_t units = a.tokens * a.parts, warps = static_cast<int64_t>(gridDim.x) * kPpWarps;
-  const int64_t per = (units + warps - 1) / warps;
-  const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kPpWarps + warp) * per;
-  const int64_t w1 = w0 + per < units ? w0 + per : units;
+  // A unit is a group of heads of a token. Each warp takes as many consecutive ones, whole tokens and parts of them, so that
+  // all warps end together and a request is looked up once for a run of its tokens.
   const int groups_q = (a.Hq + kHeads - 1) / kHeads, groups_kv = (a.Hkv + kHeads - 1) / kHeads;
   const int groups = groups_q + 2 * groups_kv;
+  const int64_t units = a.tokens * groups, warps = static_cast<int64_t>(gridDim.x) * kPpWarps;
+  int64_t per = (units + warps - 1) / warps;
+  if (per > 1) per += per & 1;  // two groups are in work at a time
+  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * kPpWarps + warp) * per;
+  const int64_t u1 = u0 + per < units ? u0 + per : units;
+  int64_t i = u0 / groups;
+  int g0 = static_cast<int>(u0 - i * groups);
   int64_t b = 0, e = 0, L = 0;
   int32_t r = 0;
-  for (int64_t w = w0; w < w1; ++w) {
-    const int64_t i = w / a.parts;
-    const int part = static_cast<int>(w - i * a.parts);
+  for (int64_t u = u0; u < u1; ++i, g0 = 0) {
+    const int g1 = u1 - u < groups - g0 ? g0 + static_cast<int>(u1 - u) : groups;
+    u += g1 - g0;
     if (i < first || i >= past) continue;  // no request's token: left as it is
     if (i < b || i >= e) {
       r = find_request(a.cu, a.batch, i);
@@ -129,10 +149,9 @@ __global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(co
     const int64_t pos = ok ? L - (e - i) : 0;
     const int32_t page = ok ? a.table[r * a.max_pages + pos / a.P] : -1;
     const bool page_ok = ok && page >= 0 && page < a.num_pages;
-    if (part == 0 && lane == 0 && !page_ok) atomicOr(a.status, ok ? HPC_DEV_BAD_PAGE : HPC_DEV_BAD_SEQLEN);
+    if (g0 == 0 && lane == 0 && !page_ok) atomicOr(a.status, ok ? HPC_DEV_BAD_PAGE : HPC_DEV_BAD_SEQLEN);
     const int tok = static_cast<int>(pos % a.P);
     const __nv_bfloat16* src = a.qkv + i * heads * D + 8 * sub;
-    const int g0 = groups * part / a.parts, g1 = groups * (part + 1) / a.parts;
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < kAngles; ++k) {
@@ -148,15 +167,18 @@ __global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(co
       const int n = kind == 0 ? a.Hq : a.Hkv;                          // heads of the kind
       const int h0 = kind == 0 ? 0 : (kind == 1 ? a.Hq : a.Hq + a.Hkv);  // the first one's place
       // y1 = inv (w1 cos x1 - w2 sin x2), y2 = inv (w2 cos x2 + w1 sin x1)
-      float w1c[8], w2s[8], w2c[8], w1s[8];
+      float2 w1c[4], w2s[4], w2c[4], w1s[4];  // w2s with its sign
       if (kind < 2) {
-        float c[8], s[8], u1[8], u2[8];
+        float2 c[4], s[4], v1[4], v2[4];
         load8(s_cos[warp] + 8 * sub, c);
         load8(s_sin[warp] + 8 * sub, s);
-        load8(s_w[kind & 1] + 8 * sub, u1);
-        load8(s_w[kind & 1] + D / 2 + 8 * sub, u2);
+        load8(s_w[kind & 1] + 8 * sub, v1);
+        load8(s_w[kind & 1] + D / 2 + 8 * sub, v2);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w1c[k] = u1[k] * c[k], w2s[k] = u2[k] * s[k], w2c[k] = u2[k] * c[k], w1s[k] = u1[k] * s[k];
+        for (int k = 0; k < 4; ++k) {
+          w1c[k] = mul2(v1[k], c[k]), w2c[k] = mul2(v2[k], c[k]), w1s[k] = mul2(v1[k], s[k]);
+          w2s[k] = mul2(v2[k], make_float2(-s[k].x, -s[k].y));
+        }
       }
       uint4 in[2][2], next[2][2];
       auto load = [&](int g, uint4 (&v)[2][2]) {
@@ -178,21 +200,23 @@ __global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(co
         for (int z = 0; z < 2; ++z) {
           const int h = (g + z) * kHeads + in_group;
           const bool live = g + z < hi && h < n;
-          float x[8], y[8];
+          float2 x[4], y[4];
           unpack8(in[z][0], x);
           unpack8(in[z][1], y);
           if (kind < 2) {
-            float ss = 0.f;
+            float2 s2 = make_float2(0.f, 0.f), t2 = s2;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+            for (int k = 0; k < 4; ++k) s2 = fma2(x[k], x[k], s2), t2 = fma2(y[k], y[k], t2);
+            float ss = (s2.x + s2.y) + (t2.x + t2.y);
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = 1.f / sqrtf(ss / D + a.eps);
+            const float inv = rsqrtf(ss * (1.f / D) + a.eps);  // 2 ulp, far below a bf16 step
+            const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float p = x[k] * inv, q = y[k] * inv;
-              x[k] = p * w1c[k] - q * w2s[k];
-              y[k] = q * w2c[k] + p * w1s[k];
+            for (int k = 0; k < 4; ++k) {
+              const float2 p = mul2(x[k], inv2), q = mul2(y[k], inv2);
+              x[k] = fma2(p, w1c[k], mul2(q, w2s[k]));
+              y[k] = fma2(q, w2c[k], mul2(p, w1s[k]));
             }
           }
           if (live && (kind == 0 || (kind == 1 && a.k_out))) {
@@ -208,11 +232,8 @@ __global__ void __launch_bounds__(kPpThreads, kPpCtas) prompt_prologue_kernel(co
             if (a.fp8) {
               const float sc = (kind == 1 ? a.k_scale : a.v_scale)[h];
               uint8_t* dst = static_cast<uint8_t*>(pages) + base;
-              *reinterpret_cast<uint2*>(dst) = make_uint2(f32x4_to_e4m3x4(x[0] / sc, x[1] / sc, x[2] / sc, x[3] / sc),
-                                                          f32x4_to_e4m3x4(x[4] / sc, x[5] / sc, x[6] / sc, x[7] / sc));
-              *reinterpret_cast<uint2*>(dst + D / 2) =
-                  make_uint2(f32x4_to_e4m3x4(y[0] / sc, y[1] / sc, y[2] / sc, y[3] / sc),
-                             f32x4_to_e4m3x4(y[4] / sc, y[5] / sc, y[6] / sc, y[7] / sc));
+              *reinterpret_cast<uint2*>(dst) = pack8_e4m3(x, sc);
+              *reinterpret_cast<uint2*>(dst + D / 2) = pack8_e4m3(y, sc);
             } else {
               __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(pages) + base;
               *reinterpret_cast<uint4*>(dst) = kind == 2 ? in[z][0] : pack8(x);
@@ -295,10 +316,7 @@ extern "C" int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   const int per_group = 512 / head_dim;  // heads a warp takes at a time
   const int groups = (num_heads + per_group - 1) / per_group + 2 * ((kv_heads + per_group - 1) / per_group);
-  int64_t parts = (8 * static_cast<int64_t>(sms) + tokens - 1) / tokens;
-  if (parts > groups) parts = groups;
-  a.parts = static_cast<int32_t>(parts < 1 ? 1 : parts);
-  int64_t blocks = (tokens * a.parts + kPpWarps - 1) / kPpWarps;
+  int64_t blocks = (tokens * groups + kPpWarps - 1) / kPpWarps;
   const int64_t cap = static_cast<int64_t>(sms) * kPpCtas;
   if (blocks > cap) blocks = cap;
   auto kern = head_dim == 128 ? prompt_prologue_kernel<128> : prompt_prologue_kernel<64>;

@@ -114,6 +114,26 @@ def test_one_token_prompts_are_the_decode_prologue(B):
     assert torch.equal(d["v"], e["v"])
 
 
+def test_values_of_every_size_into_an_e4m3_cache(B):
+    """V is only divided by its scale: against the quotient in fp32, infinities, NaN, overflow and small scales included."""
+    n, Hkv, D, P = 512, 2, 128, 64
+    g = torch.Generator().manual_seed(11)
+    bits = torch.randint(0, 65536, (n, 3 * Hkv, D), generator=g, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    near = torch.randn((n, 3 * Hkv, D), generator=g).to(torch.bfloat16)
+    c = make((n,), (0,), Hkv, Hkv, D, P, "e4m3", "NHD", seed=2)
+    for x in (bits, near):
+        for vs in (torch.tensor([0.37, 3.1]), torch.tensor([1e-6, 2.0 ** -9]), torch.tensor([0.0117, 1e4])):
+            c["qkv"], c["vs"] = x, vs
+            d, _, _, st = run(B, c, Hkv, Hkv, "e4m3", "NHD")
+            assert st == 0
+            y = x[:, 2 * Hkv:].float() / vs[:, None]
+            got = d["v"].cpu()[c["table"][0, :n // P].long()].reshape(n, Hkv, D)
+            nan = y.isnan()
+            assert torch.equal((got & 127) == 127, nan)
+            codes = torch.from_numpy(OF.encode_array(y.double().nan_to_num(0).clamp(-448, 448).numpy()).astype(np.uint8))
+            assert torch.equal(got[~nan], codes[~nan])
+
+
 def test_padded_rows_are_left_alone(B):
     Hq, Hkv, D, P = 8, 2, 64, 16
     c = make((5, 9), (0, 3), Hq, Hkv, D, P, "bf16", "HND", pad=(2, 6))
