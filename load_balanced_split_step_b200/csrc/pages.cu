@@ -16,8 +16,7 @@
 //
 // The data is moved by pages_copy_kernel, for any number of caches (the K and V of every layer
 // share the table), from the list a planner leaves on the device. A destination was free and a
-// source is live, so no page is both. 16 bytes a thread, four loads in flight, 8 CTAs of 256 threads per SM: 268 MB in
-// 98 us with a planner ahead (5.5 TB/s of reads and writes).
+// source is live, so no page is both.
 //
 // The planners are bound by latency (about eight dependent accesses and three to four barriers) and, in large pools, by
 // what eight SMs copy: a resize of 256 requests in a pool of 40000 pages takes 11.5 us, of 4 requests in one of 512
@@ -540,7 +539,8 @@ __global__ void __cluster_dims__(kPgCtas, 1, 1) __launch_bounds__(kPgThreads, 1)
 
 // ---- copy -------------------------------------------------------------------------------
 constexpr int kPgCopyThreads = 256;
-constexpr int kPgCopyVecs = 4;  // 16-byte loads in flight per thread
+constexpr int kPgCopyVecs = 8;  // 16-byte loads in flight per thread
+constexpr int kPgCopyCtas = 8;  // per SM
 constexpr int kPgCopyChunk = kPgCopyThreads * kPgCopyVecs;
 constexpr int kPgMaxCaches = 256;  // pointers in one launch's parameters
 
@@ -548,7 +548,9 @@ struct PgCaches {
   uint4* base[kPgMaxCaches];
 };
 
-// Work is (move, cache, 16 KB chunk of the page), dealt over a persistent grid in that order.
+// Work is (move, cache, 32 KB chunk of the page), dealt over the grid in that order. Of the 8 CTAs for each SM five fit at
+// a time; the others even the work out. 268 MB read and written in 88 us (with four loads a thread, all CTAs resident, 96;
+// with 32 CTAs for each SM 85, but a call that finds nothing to copy takes 6.3 instead of 3.1).
 __global__ void __launch_bounds__(kPgCopyThreads)
     pages_copy_kernel(const __grid_constant__ PgCaches caches, int32_t n_caches, int64_t page_vecs, int32_t num_pages,
                       const int2* moves, const int32_t* n_moves, int32_t capacity, uint32_t* status) {
@@ -718,13 +720,13 @@ extern "C" int hpc_pages_copy(void* const* caches, int32_t n_caches, int64_t pag
   const int64_t page_vecs = page_bytes / 16;
   const int64_t chunks = (page_vecs + kPgCopyChunk - 1) / kPgCopyChunk;
   const int sms = device_sm_count();
-  const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 148) * (2048 / kPgCopyThreads);
+  const int64_t cap = static_cast<int64_t>(sms > 0 ? sms : 148) * kPgCopyCtas;
   for (int32_t c0 = 0; c0 < n_caches; c0 += kPgMaxCaches) {
     PgCaches list = {};
     const int32_t nc = n_caches - c0 < kPgMaxCaches ? n_caches - c0 : kPgMaxCaches;
     for (int32_t i = 0; i < nc; ++i) list.base[i] = static_cast<uint4*>(caches[c0 + i]);
     const int64_t most = chunks * nc * move_capacity;  // the count itself is on the device
-    const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(most < resident ? most : resident)),
+    const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(most < cap ? most : cap)),
                                      dim3(kPgCopyThreads), 0, static_cast<cudaStream_t>(stream), list, nc, page_vecs,
                                      num_pages, reinterpret_cast<const int2*>(moves), n_moves, move_capacity, status);
     if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "pages_copy_kernel: %s", cudaGetErrorString(e));
