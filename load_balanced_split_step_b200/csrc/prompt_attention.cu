@@ -23,7 +23,9 @@
 //
 // Persistent CTAs (one per SM) take units longest first from a counter: units are put in 64 buckets by the number
 // of keys they reach, in a table that every CTA builds from cu_seqlens at the start. (Where there is a CTA for every
-// unit they are dealt as they come: without the table a prompt of 200 tokens takes 11.3 us instead of 12.5.)
+// unit they are dealt as they come, without the table: a prompt of 200 tokens takes 11.3 us instead of 12.5. Where there
+// is one for every tile, a unit is one tile, which does not wait for another's scores: 10.3 us; 1024 tokens of 8/8
+// heads 17.8 instead of 20.4.)
 // Where a bucket's units are longer than a CTA's share of all blocks (few heads, or a few new tokens on a long
 // cache), they are cut into parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second
 // kernel, launched behind this one, joins them (a last part that joined the others by itself took 40 us for 18 parts
@@ -114,6 +116,7 @@ struct PaArgs {
   float scale_log2, scale;
   int32_t batch, Hq, Hkv, group, causal, P, num_pages, nhd, slots;
   int32_t unsorted;  // a CTA for every unit: they are dealt as they come
+  int32_t single;    // so few that a unit is one tile: A, and no B
 };
 
 struct PaBars {
@@ -269,8 +272,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + L::kOffRing;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group_shift = 31 - __clz(a.group), unit_shift = 8 - group_shift;  // 1, 2, 4 or 8 heads
-  const int32_t tokens_per_unit = 1 << unit_shift, tokens_per_tile = tokens_per_unit / 2;
+  const int group_shift = 31 - __clz(a.group), unit_shift = 8 - group_shift - a.single;  // 1, 2, 4 or 8 heads
+  const int32_t tokens_per_unit = 1 << unit_shift, tokens_per_tile = kPaRows >> group_shift;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
   if (threadIdx.x == 0) {
@@ -706,6 +709,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 if (seen > keys) seen = keys;
                 x.blocks[t] = first < q1 && seen > 0 ? (seen + kPaKeys - 1) / kPaKeys : 0;
               }
+              if (a.single) x.blocks[1] = 0;
               // the part's blocks
               int32_t length = x.blocks[0] > x.blocks[1] ? x.blocks[0] : x.blocks[1];
               if (parts > 1) {
@@ -718,6 +722,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                 x.parts[t] = parts > 1 ? (have + length - 1) / length : (have > 0 ? 1 : 0);
                 x.blocks[t] = left < 0 ? 0 : (left < length ? left : length);
               }
+              if (a.single) x.parts[1] = 1;  // the tile is another unit's
               break;
             }
             const int32_t sum = __shfl_sync(0xffffffffu, inc, 31);
@@ -749,10 +754,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (!ok) break;
         ++n_q;
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(sh.bars.q_full), 2 * L::kTile);
+          mbar_arrive_expect_tx(bar(sh.bars.q_full), a.single ? L::kTile : 2 * L::kTile);
+#pragma unroll
           for (int t = 0; t < 2; ++t)
+#pragma unroll
             for (int pl = 0; pl < L::kPlanes; ++pl)
-              tma_load_4d(smem_u32(smem) + t * L::kTile + pl * kPaPlane, &tm_q, bar(sh.bars.q_full), 64 * pl,
+              if (t == 0 || !a.single)
+                tma_load_4d(smem_u32(smem) + t * L::kTile + pl * kPaPlane, &tm_q, bar(sh.bars.q_full), 64 * pl,
                           x.kvh * a.group, x.q0 + t * tokens_per_tile, 0);
         }
         // K_0, V_0, K_1, V_1, ...
@@ -1071,11 +1079,12 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-  // units: at most one part-filled per sequence and kv head
-  const int64_t per_unit = 2 * kPaRows / a.group;
-  const int64_t most = (a.tokens / per_unit + (a.batch < a.tokens ? a.batch : a.tokens)) * a.Hkv;
-  const int grid = a.slots > 0 ? sms : static_cast<int>(most < sms ? most : sms);
+  // units of one or two tiles: at most one part-filled per sequence and kv head
+  auto units = [&](int64_t rows) { return (a.tokens / (rows / a.group) + (a.batch < a.tokens ? a.batch : a.tokens)) * a.Hkv; };
+  a.single = a.slots == 0 && units(kPaRows) <= sms;
+  const int64_t most = units(a.single ? kPaRows : 2 * kPaRows);
   a.unsorted = a.slots == 0 && most <= sms;
+  const int grid = a.slots > 0 ? sms : static_cast<int>(most < sms ? most : sms);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kPaThreads), static_cast<size_t>(L::kBytes), stream, q, k, v, a);
   if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_attention_kernel: %s", cudaGetErrorString(e));
   const int rc = check_launch("prompt_attention_kernel");
