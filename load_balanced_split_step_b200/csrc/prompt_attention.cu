@@ -24,14 +24,17 @@
 // Persistent CTAs (one per SM) take units longest first from a counter: units are put in 64 buckets by the number
 // of keys they reach, in a table that every CTA builds from cu_seqlens at the start. (Where there is a CTA for every
 // unit they are dealt as they come, without the table: a prompt of 200 tokens takes 11.3 us instead of 12.5. Where there
-// is one for every tile, a unit is one tile, which does not wait for another's scores: 10.3 us; 1024 tokens of 8/8
-// heads 17.8 instead of 20.4.)
+// is one for every tile (or two, if units may be cut), a unit is one tile, which does not wait for another's scores:
+// 10.3 us; 1024 tokens of 8/8 heads 17.8 instead of 20.4.)
 // Where a bucket's units are longer than a CTA's share of all blocks (few heads, or a few new tokens on a long
 // cache), they are cut into parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second
 // kernel, launched behind this one, joins them (a last part that joined the others by itself took 40 us for 18 parts
 // of a tile: one SM reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut,
 // 39 us so. A part has 6 blocks at least: of 2, 3, 4, 6 and 9
 // that loses least over nine shapes (mixed lengths on 9000 keys 53 us at 2, 47 at 6, 41 at 9; 800 on 1800 keys 22, 25, 29).
+// Cutting has to save 5 blocks, and where it makes up to a third more parts than CTAs, the parts are made longer instead
+// (1700 tokens of 16/8 heads 46.8 us without the two, 39.1 with; 900 on 2400 keys 51.9 and 45.8; the worst of twenty
+// shapes 23.9 and 25.6).
 // The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
 // (swizzled planes of 64 elements). The next unit's Q has to wait for its place, and comes as far as L2 meanwhile
 // (its arrival after that took 3000 cycles, now 1400).
@@ -65,6 +68,7 @@ constexpr float kPaMove = 8.f;
 constexpr int kPaSplit = 2;               // P is handed over in two parts: after 64 keys, and whole
 constexpr int kPaStages64 = 8, kPaStages128 = 5;
 constexpr int kPaMinPart = 6;           // blocks: joining costs more than shorter parts save
+constexpr int kPaMinSave = 5;           // blocks that cutting has to save
 constexpr int kPaMaxParts = 32;
 constexpr int kPaCuts = 512;            // cut units that the scratch can describe, ahead of the slots
 
@@ -373,21 +377,29 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // Parts per unit: about a CTA's share of all blocks each, as long as the scratch has a place for them. The
         // buckets that are cut come first, so that a part's number is its place.
         const float share = static_cast<float>(sh.blocks) * a.Hkv / gridDim.x;  // the same in every CTA
-        const int32_t length = share > kPaMinPart ? static_cast<int32_t>(fminf(ceilf(share), 1e9f)) : kPaMinPart;
-        auto cut = [&](int b) -> int32_t {
-          const int64_t most = (((static_cast<int64_t>(b + 1) << bucket) + 1) << unit_shift) / kPaKeys + 1,
-                        least = ((static_cast<int64_t>(b) << bucket) << unit_shift) / kPaKeys;
-          // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
-          if (10 * most <= 13ll * length || 2 * least < length) return 1;
-          const float n = ceilf(static_cast<float>(most) / static_cast<float>(length));
-          return n < kPaMaxParts ? static_cast<int32_t>(n) : kPaMaxParts;
-        };
+        int32_t length = share > kPaMinPart ? static_cast<int32_t>(fminf(ceilf(share), 1e9f)) : kPaMinPart;
+      auto cut = [&](int b) -> int32_t {
+        const int64_t most = (((static_cast<int64_t>(b + 1) << bucket) + 1) << unit_shift) / kPaKeys + 1,
+                      least = ((static_cast<int64_t>(b) << bucket) << unit_shift) / kPaKeys;
+        // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
+        if (10 * most <= 13ll * length || most < length + kPaMinSave || 2 * least < length) return 1;
+        const float n = ceilf(static_cast<float>(most) / static_cast<float>(length));
+        return n < kPaMaxParts ? static_cast<int32_t>(n) : kPaMaxParts;
+      };
+      const int32_t room = a.slots / a.Hkv;
+      int32_t end = 0;
+      for (int again = 0; again < 2; ++again) {
         p0 = cut(b0), p1 = cut(b1);
-        const int32_t room = a.slots / a.Hkv, end = scan(c0 * p0 + c1 * p1);
-        if (end - c1 * p1 > room) p0 = 1;
-        if (end > room) p1 = 1;
+        end = scan(c0 * p0 + c1 * p1);
+        // a few parts more than CTAs would take a second turn: rather longer parts
+        const int64_t all = static_cast<int64_t>(__shfl_sync(0xffffffffu, end, 31)) * a.Hkv;
+        if (all <= gridDim.x || 20 * all > 27ll * gridDim.x) break;
+        length = static_cast<int32_t>((static_cast<int64_t>(length) * all + gridDim.x - 1) / gridDim.x);
       }
-      const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
+      if (end - c1 * p1 > room) p0 = 1;
+      if (end > room) p1 = 1;
+    }
+    const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
       sh.parts[b0] = p0;
       sh.parts[b1] = p1;
       sh.count[b0] = n0;
@@ -1081,7 +1093,7 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
   // units of one or two tiles: at most one part-filled per sequence and kv head
   auto units = [&](int64_t rows) { return (a.tokens / (rows / a.group) + (a.batch < a.tokens ? a.batch : a.tokens)) * a.Hkv; };
-  a.single = a.slots == 0 && units(kPaRows) <= sms;
+  a.single = units(kPaRows) <= (a.slots > 0 ? sms / 2 : sms);
   const int64_t most = units(a.single ? kPaRows : 2 * kPaRows);
   a.unsorted = a.slots == 0 && most <= sms;
   const int grid = a.slots > 0 ? sms : static_cast<int>(most < sms ? most : sms);
