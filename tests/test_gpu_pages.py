@@ -83,6 +83,49 @@ def test_resize(B, shape, share, inplace):
         assert np.array_equal(want[1], OP.counts(want[0], new, N, P))
 
 
+@pytest.mark.parametrize("N,taken", [(70000, 0.97), (150000, 0.5), (65537, 0.999)])
+def test_a_crowded_large_pool(B, N, taken):
+    """Most pages are held elsewhere, so that the pages that are taken lie far apart, in every part of a warp's run."""
+    rng = np.random.default_rng(N)
+    rows, M, P = 60, 40, 16
+    ref = (rng.random(N) < taken).astype(np.int32)
+    table = np.full((rows, M), -1, dtype=np.int32)
+    lens = rng.integers(1, M * P // 2, rows).astype(np.int32)
+    held = rng.permutation(np.flatnonzero(ref == 0))
+    o = 0
+    for r, n in enumerate(lens):
+        h = min(OP.held(n, P), max(1, (len(held) - o) // (2 * (rows - r))))
+        lens[r] = min(n, h * P)
+        table[r, :h] = held[o:o + h]
+        ref[held[o:o + h]] = 1
+        o += h
+    free = int((ref == 0).sum())
+    new = np.minimum(lens + rng.integers(0, max(2, free * P // rows), rows), M * P).astype(np.int32)
+    t, l, n, c = dev(table, lens, new, ref)
+    want = OP.resize(table, lens, new, ref, P)
+    up = B.resize_pages(t, l, n, c, P)
+    assert int(up.status.item()) == (B.DEV_STATUS["capacity"] if want is None else 0)
+    if want is None:
+        same(up.block_table, table)
+        same(up.ref_count, ref)
+    else:
+        same(up.block_table, want[0])
+        same(up.ref_count, want[1])
+        par = rng.integers(0, rows, rows).astype(np.int32)
+        want = OP.fork(want[0], new, want[1], par, P)
+        up = B.fork_pages(up.block_table, n, up.ref_count, dev(par)[0], P)
+        assert int(up.status.item()) == (B.DEV_STATUS["capacity"] if want is None else 0)
+        if want is not None:
+            same(up.block_table, want[0])
+            same(up.ref_count, want[2])
+            assert moves_of(up) == want[3]
+    want = OP.compact(table, ref)
+    up = B.compact_pages(t, c)
+    same(up.block_table, want[0])
+    same(up.ref_count, want[1])
+    assert moves_of(up) == want[3]
+
+
 def test_resize_copies_a_shared_part_filled_page_on_write(B):
     """Both sharers of a part-filled page grow in one call: each takes a copy, the page itself is left
     free, and it is not taken in the same call."""
