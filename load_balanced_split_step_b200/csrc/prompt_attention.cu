@@ -30,11 +30,11 @@
 // cache), they are cut into parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second
 // kernel, launched behind this one, joins them (a last part that joined the others by itself took 40 us for 18 parts
 // of a tile: one SM reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut,
-// 39 us so. A part has 6 blocks at least: of 2, 3, 4, 6 and 9
+// 41 us so. A part has 6 blocks at least: of 2, 3, 4, 6 and 9
 // that loses least over nine shapes (mixed lengths on 9000 keys 53 us at 2, 47 at 6, 41 at 9; 800 on 1800 keys 22, 25, 29).
 // Cutting has to save 5 blocks, and where it makes up to a third more parts than CTAs, the parts are made longer instead
 // (1700 tokens of 16/8 heads 46.8 us without the two, 39.1 with; 900 on 2400 keys 51.9 and 45.8; the worst of twenty
-// shapes 23.9 and 25.6).
+// shapes 23.9 and 25.6; all with half the CTAs that join now).
 // The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
 // (swizzled planes of 64 elements). The next unit's Q has to wait for its place, and comes as far as L2 meanwhile
 // (its arrival after that took 3000 cycles, now 1400).
@@ -985,8 +985,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
 // Joins the parts of cut units by log-sum-exp: M = max m_i, w_i = 2^(c (m_i - M)), out = sum w_i O_i / sum w_i l_i.
 // A block takes four columns of a tile, a thread per row, so that the parts are read side by side and the whole
-// GPU reads them. Parts are added in order: the same result every time.
-constexpr int kPaJoin = 8;  // parts loaded together
+// GPU reads them. Parts are added in order: the same result every time. With 4 CTAs for each SM a call of 900 queries on 2400
+// keys of 16/2 heads takes 46 us, with 8 of them 38, with 16 36; where nothing is cut 16 take 1 us more.
+constexpr int kPaJoin = 8;      // parts loaded together
+constexpr int kPaJoinCtas = 8;  // per SM: all that fit
 template <int D>
 __global__ void __launch_bounds__(kPaRows) prompt_join_kernel(const PaArgs a) {
   pdl_wait();
@@ -1101,7 +1103,7 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
   if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_attention_kernel: %s", cudaGetErrorString(e));
   const int rc = check_launch("prompt_attention_kernel");
   if (rc != HPC_OK || a.slots == 0) return rc;
-  const cudaError_t j = launch_pdl(prompt_join_kernel<D>, dim3(4 * sms), dim3(kPaRows), 0, stream, a);
+  const cudaError_t j = launch_pdl(prompt_join_kernel<D>, dim3(kPaJoinCtas * sms), dim3(kPaRows), 0, stream, a);
   if (j != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_join_kernel: %s", cudaGetErrorString(j));
   return check_launch("prompt_join_kernel");
 }
