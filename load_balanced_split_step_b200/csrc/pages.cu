@@ -605,7 +605,8 @@ int check_rows(int32_t rows, int32_t max_pages, int32_t page_size) {
 }
 
 int launch_planner(void (*kernel)(PgArgs), const char* name, const PgArgs& args, size_t smem, void* stream) {
-  if (smem > 48 * 1024 &&
+  // Without the attribute a block has 48 KB, the kernel's own variables (below 1 KB) among them.
+  if (smem + 1024 > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return check_launch(name);
   const cudaError_t e = launch_pdl(kernel, dim3(kPgCtas), dim3(kPgThreads), smem, static_cast<cudaStream_t>(stream), args);
