@@ -27,10 +27,10 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-int check_launch(const char* what) {
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  return HPC_OK;
+int launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return HPC_OK;
+  cudaGetLastError();
+  return fail(HPC_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
 int device_sm_count() {
@@ -100,6 +100,11 @@ extern "C" int hpc_wait_selftest(uint64_t limit_ns, int32_t arrive, uint32_t* st
   if (!status) return fail(HPC_ERR_ARG, "null pointer argument");
   if (limit_ns == 0 || limit_ns > kWaitLimitNs)
     return fail(HPC_ERR_ARG, "limit_ns must be in 1 .. %llu", static_cast<unsigned long long>(kWaitLimitNs));
-  wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns, arrive != 0, status, waited_ns);
-  return check_launch("wait_selftest_kernel");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(32);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, wait_selftest_kernel, limit_ns, static_cast<int>(arrive != 0), status, waited_ns);
+  return launched(e, "wait_selftest_kernel");
 }

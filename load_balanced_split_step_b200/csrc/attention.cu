@@ -913,13 +913,12 @@ int launch(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& prm, 
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && configured[dev] < smem) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return check_launch("cudaFuncSetAttribute(decode_attention_kernel)");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return launched(e, "cudaFuncSetAttribute(decode_attention_kernel)");
     configured[dev] = smem;
   }
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), static_cast<size_t>(smem), stream, mk, mv, prm);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "decode_attention_kernel: %s", cudaGetErrorString(e));
-  return check_launch("decode_attention_kernel");
+  return launched(e, "decode_attention_kernel");
 }
 
 }  // namespace

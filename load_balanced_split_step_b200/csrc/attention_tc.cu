@@ -685,13 +685,12 @@ int launch_attention_tc(bool fused, const CUtensorMap& mk, const CUtensorMap& mv
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && configured[fused][dev] < smem) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return check_launch("cudaFuncSetAttribute(decode_attention_tc_kernel)");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return launched(e, "cudaFuncSetAttribute(decode_attention_tc_kernel)");
     configured[fused][dev] = smem;
   }
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kTcThreads), static_cast<size_t>(smem), stream, mk, mv, p);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "decode_attention_tc_kernel: %s", cudaGetErrorString(e));
-  return check_launch("decode_attention_tc_kernel");
+  return launched(e, "decode_attention_tc_kernel");
 }
 
 }  // namespace attn

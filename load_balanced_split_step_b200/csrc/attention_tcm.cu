@@ -790,15 +790,14 @@ int launch_attention_tcm(const CUtensorMap& mk, const CUtensorMap& mv, const Att
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !configured[dev]) {
-    if (cudaFuncSetAttribute(decode_attention_tcm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmSmem) !=
-        cudaSuccess)
-      return check_launch("cudaFuncSetAttribute(decode_attention_tcm_kernel)");
+    const cudaError_t e =
+        cudaFuncSetAttribute(decode_attention_tcm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmSmem);
+    if (e != cudaSuccess) return launched(e, "cudaFuncSetAttribute(decode_attention_tcm_kernel)");
     configured[dev] = 1;
   }
   const cudaError_t e = launch_pdl(decode_attention_tcm_kernel, dim3(grid), dim3(kTmThreads),
                                    static_cast<size_t>(kTmSmem), stream, mk, mv, prm);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "decode_attention_tcm_kernel: %s", cudaGetErrorString(e));
-  return check_launch("decode_attention_tcm_kernel");
+  return launched(e, "decode_attention_tcm_kernel");
 }
 
 }  // namespace attn

@@ -180,6 +180,5 @@ extern "C" int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_d
                               : (fp8 ? gather_tokens_kernel<64, true> : gather_tokens_kernel<64, false>);
   const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kGtThreads),
                                    (static_cast<size_t>(batch) + 1) * 4, static_cast<cudaStream_t>(stream), a);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "gather_tokens_kernel: %s", cudaGetErrorString(e));
-  return check_launch("gather_tokens_kernel");
+  return launched(e, "gather_tokens_kernel");
 }

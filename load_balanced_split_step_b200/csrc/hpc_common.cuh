@@ -18,7 +18,10 @@ namespace hpc {
 // ---------------------------------------------------------------------------------------
 void set_error(const char* fmt, ...);  // thread-local message read by hpc_last_error()
 int fail(int code, const char* fmt, ...);
-int check_launch(const char* what);  // cudaGetLastError() after a launch
+// HPC_OK, or HPC_ERR_CUDA for what a launch (or an attribute set before one) returned. The runtime keeps a failed call's
+// error as its last one; it is cleared here, and no launch is judged by it: a call after a failed one that was
+// caught is not reported as failed when its kernel runs.
+int launched(cudaError_t e, const char* what);
 int device_sm_count();                 // SMs of the current device (cached per device)
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -121,10 +121,8 @@ extern "C" int hpc_merge_states(const float* partial_o, const float* partial_ml,
   int grid = plan->is_static ? plan->merge_capacity : plan->num_ctas;
   if (grid > 2 * sms) grid = 2 * sms;
   if (grid < 1) grid = 1;
-  const cudaError_t e =
-      launch_pdl(merge_states_kernel, dim3(grid), dim3(kMergeThreads), 0, static_cast<cudaStream_t>(stream), partial_o,
+  const cudaError_t e = launch_pdl(merge_states_kernel, dim3(grid), dim3(kMergeThreads), 0, static_cast<cudaStream_t>(stream), partial_o,
                  partial_ml, plan->merge_list, plan->merge_indptr, plan->counts, plan->kv_heads, group, head_dim,
                  num_heads, out, static_cast<int>(out_dtype == HPC_BF16));
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "merge_states_kernel: %s", cudaGetErrorString(e));
-  return check_launch("merge_states_kernel");
+  return launched(e, "merge_states_kernel");
 }

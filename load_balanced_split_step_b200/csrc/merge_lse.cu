@@ -162,8 +162,7 @@ extern "C" int hpc_merge_lse(const float* outs, const float* lses, int32_t parts
   if (blocks > cap) blocks = cap;
   const cudaError_t e = launch_pdl(merge_lse_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeLseThreads), 0,
                                    static_cast<cudaStream_t>(stream), outs, lses, parts, rows, head_dim, out, lse_out);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "merge_lse_kernel: %s", cudaGetErrorString(e));
-  return check_launch("merge_lse_kernel");
+  return launched(e, "merge_lse_kernel");
 }
 
 extern "C" int hpc_merge_lse_gather(const float* outs, const float* lses, int64_t part_rows, const int32_t* part_index,
@@ -179,12 +178,10 @@ extern "C" int hpc_merge_lse_gather(const float* outs, const float* lses, int64_
   const int sms = device_sm_count();
   const int64_t cap = sms > 0 ? static_cast<int64_t>(sms) * 8 : 1024;
   if (blocks > cap) blocks = cap;
-  const cudaError_t e =
-      launch_pdl(merge_lse_gather_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeLseThreads), 0,
+  const cudaError_t e = launch_pdl(merge_lse_gather_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeLseThreads), 0,
                  static_cast<cudaStream_t>(stream), outs, lses, part_index, max_parts, part_rows, batch, num_heads,
                  head_dim, out, lse_out, status);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "merge_lse_gather_kernel: %s", cudaGetErrorString(e));
-  return check_launch("merge_lse_gather_kernel");
+  return launched(e, "merge_lse_gather_kernel");
 }
 
 extern "C" int hpc_gather_rows(const void* src, int64_t src_rows, int64_t row_bytes, const int32_t* index, int64_t n,
@@ -200,12 +197,10 @@ extern "C" int hpc_gather_rows(const void* src, int64_t src_rows, int64_t row_by
   const int sms = device_sm_count();
   const int64_t cap = sms > 0 ? static_cast<int64_t>(sms) * 8 : 1024;
   if (blocks > cap) blocks = cap;
-  const cudaError_t e =
-      launch_pdl(gather_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeLseThreads), 0,
+  const cudaError_t e = launch_pdl(gather_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeLseThreads), 0,
                  static_cast<cudaStream_t>(stream), static_cast<const uint4*>(src), src_rows, index, n, row_vecs,
                  static_cast<uint4*>(dst), status);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "gather_rows_kernel: %s", cudaGetErrorString(e));
-  return check_launch("gather_rows_kernel");
+  return launched(e, "gather_rows_kernel");
 }
 
 extern "C" int hpc_gather_pages(const int32_t* src, int32_t src_rows, int32_t src_cols, const int32_t* req,
@@ -222,6 +217,5 @@ extern "C" int hpc_gather_pages(const int32_t* src, int32_t src_rows, int32_t sr
   const cudaError_t e = launch_pdl(gather_pages_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeLseThreads), 0,
                                    static_cast<cudaStream_t>(stream), src, src_rows, src_cols, req, col0, n, width,
                                    dst, status);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "gather_pages_kernel: %s", cudaGetErrorString(e));
-  return check_launch("gather_pages_kernel");
+  return launched(e, "gather_pages_kernel");
 }

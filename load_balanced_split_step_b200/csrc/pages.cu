@@ -606,12 +606,12 @@ int check_rows(int32_t rows, int32_t max_pages, int32_t page_size) {
 
 int launch_planner(void (*kernel)(PgArgs), const char* name, const PgArgs& args, size_t smem, void* stream) {
   // Without the attribute a block has 48 KB, the kernel's own variables (below 1 KB) among them.
-  if (smem + 1024 > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return check_launch(name);
+  if (smem + 1024 > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return launched(e, name);
+  }
   const cudaError_t e = launch_pdl(kernel, dim3(kPgCtas), dim3(kPgThreads), smem, static_cast<cudaStream_t>(stream), args);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
-  return check_launch(name);
+  return launched(e, name);
 }
 
 }  // namespace
@@ -730,8 +730,7 @@ extern "C" int hpc_pages_copy(void* const* caches, int32_t n_caches, int64_t pag
     const cudaError_t e = launch_pdl(pages_copy_kernel, dim3(static_cast<unsigned>(most < cap ? most : cap)),
                                      dim3(kPgCopyThreads), 0, static_cast<cudaStream_t>(stream), list, nc, page_vecs,
                                      num_pages, reinterpret_cast<const int2*>(moves), n_moves, move_capacity, status);
-    if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "pages_copy_kernel: %s", cudaGetErrorString(e));
-    const int rc = check_launch("pages_copy_kernel");
+    const int rc = launched(e, "pages_copy_kernel");
     if (rc != HPC_OK) return rc;
   }
   return HPC_OK;

@@ -348,8 +348,7 @@ extern "C" int hpc_decode_plan(const int32_t* seq_lens, int32_t batch, int32_t n
   const cudaError_t e = launch_pdl(dynamic_plan_kernel, dim3(1), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream),
                                    seq_lens, batch, kv_heads, tile_len, num_ctas, max_seq_len,
                                    static_cast<int32_t>(max_items), ptrs_of(plan), status);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "dynamic_plan_kernel: %s", cudaGetErrorString(e));
-  return check_launch("dynamic_plan_kernel");
+  return launched(e, "dynamic_plan_kernel");
 }
 
 extern "C" int hpc_decode_plan_static(const int32_t* seq_lens, int32_t batch, int32_t num_heads, int32_t kv_heads,
@@ -366,8 +365,7 @@ extern "C" int hpc_decode_plan_static(const int32_t* seq_lens, int32_t batch, in
   bind_plan(workspace, L, batch, kv_heads, tile_len, static_cast<int32_t>(G), static_cast<int32_t>(G), 1, plan);
   const cudaError_t e = launch_pdl(static_plan_kernel, dim3(1), dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream),
                                    seq_lens, batch, kv_heads, tile_len, splits, max_seq_len, ptrs_of(plan), status);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "static_plan_kernel: %s", cudaGetErrorString(e));
-  return check_launch("static_plan_kernel");
+  return launched(e, "static_plan_kernel");
 }
 
 // Host twin: the same closed form, evaluated sequentially.

@@ -128,6 +128,5 @@ extern "C" int hpc_decode_prologue(const void* qkv, const float* q_norm_w, const
                                    k_scale, v_scale, num_pages, page_size, block_table,
                                    static_cast<int64_t>(max_pages_per_req), seq_lens, num_heads, kv_heads,
                                    static_cast<int>(kv_layout == HPC_NHD), status);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prologue_kernel: %s", cudaGetErrorString(e));
-  return check_launch("prologue_kernel");
+  return launched(e, "prologue_kernel");
 }

@@ -1088,8 +1088,8 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
   cudaGetDevice(&dev);
   auto kern = prompt_attention_kernel<D, kPaged>;
   if (dev < 0 || dev >= 64 || !configured[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
-      return check_launch("cudaFuncSetAttribute(prompt_attention_kernel)");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return launched(e, "cudaFuncSetAttribute(prompt_attention_kernel)");
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
   const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
@@ -1100,12 +1100,10 @@ int pa_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, 
   a.unsorted = a.slots == 0 && most <= sms;
   const int grid = a.slots > 0 ? sms : static_cast<int>(most < sms ? most : sms);
   const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kPaThreads), static_cast<size_t>(L::kBytes), stream, q, k, v, a);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_attention_kernel: %s", cudaGetErrorString(e));
-  const int rc = check_launch("prompt_attention_kernel");
+  const int rc = launched(e, "prompt_attention_kernel");
   if (rc != HPC_OK || a.slots == 0) return rc;
   const cudaError_t j = launch_pdl(prompt_join_kernel<D>, dim3(kPaJoinCtas * sms), dim3(kPaRows), 0, stream, a);
-  if (j != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_join_kernel: %s", cudaGetErrorString(j));
-  return check_launch("prompt_join_kernel");
+  return launched(j, "prompt_join_kernel");
 }
 
 size_t pa_slot_bytes(int32_t head_dim) { return static_cast<size_t>(2) * kPaRows * (head_dim + 2) * sizeof(float); }

@@ -322,6 +322,5 @@ extern "C" int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_
   auto kern = head_dim == 128 ? prompt_prologue_kernel<128> : prompt_prologue_kernel<64>;
   const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kPpThreads), 0,
                                    static_cast<cudaStream_t>(stream), a);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "prompt_prologue_kernel: %s", cudaGetErrorString(e));
-  return check_launch("prompt_prologue_kernel");
+  return launched(e, "prompt_prologue_kernel");
 }

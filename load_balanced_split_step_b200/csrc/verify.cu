@@ -342,6 +342,5 @@ extern "C" int hpc_verify_drafts(const int32_t* draft_tokens, const void* target
   while (ctas > 1 && static_cast<int64_t>(batch) * ctas > room) ctas /= 2;
   const cudaError_t e = prob_dtype == HPC_FP32 ? launch_verify<float>(a, batch, ctas, st)
                                                : launch_verify<__nv_bfloat16>(a, batch, ctas, st);
-  if (e != cudaSuccess) return fail(HPC_ERR_CUDA, "verify_kernel: %s", cudaGetErrorString(e));
-  return check_launch("verify_kernel");
+  return launched(e, "verify_kernel");
 }
