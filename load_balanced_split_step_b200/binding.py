@@ -152,11 +152,8 @@ _FAST_CALLS = ("hpc_prompt_prologue", "hpc_prompt_attention", "hpc_prompt_attent
 
 def _bind(lib):
     if _fast is not None:
-        _fast.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_CALLS))
+        _fast.bind(_check, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _FAST_CALLS))
     return lib
-
-
-_lib = _bind(_load())
 
 
 def use_library(path: str = LIB):
@@ -178,6 +175,9 @@ def status_string(code: int) -> str:
 def _check(rc: int, what: str):
     if rc != HPC_OK:
         raise HpcError(f"{what}: {status_string(rc)} ({rc}): {_lib.hpc_last_error().decode()}")
+
+
+_lib = _bind(_load())
 
 
 def _ptr(t):

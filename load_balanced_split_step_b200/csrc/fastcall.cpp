@@ -4,8 +4,9 @@
 // several times the kernels of a small call. This module does the same for calls in the common form: all
 // tensors plain CUDA tensors of the expected types and shapes on the current device, outside a graph
 // capture where it would have to make a status word. It returns None for every other call, and when the
-// library refuses one; binding.py then goes its own way, with its checks and its messages. Nothing is
-// launched before a None.
+// library refuses one for its arguments; binding.py then goes its own way, with its checks and its messages. Nothing is
+// launched before a None: an error of the launches themselves is raised here, since a second try would run a call twice
+// of which a part has run.
 //
 // The library's functions are given by address (bind), so that another build of it can be switched to.
 #include <ATen/ATen.h>
@@ -39,8 +40,17 @@ struct Api {
   decltype(&hpc_prompt_attention_partial_bytes) partial_bytes;
 } api = {};
 
+// binding._check: raises the error of a library call, given its return code and name.
+PyObject* check = nullptr;
+
 // Thrown for whatever is not the common form.
 struct NotCommon {};
+// Thrown when the library could not launch.
+struct NotLaunched {
+  int rc;
+  const char* name;
+};
+bool accepted = false;  // the library has taken this call: there is no other way for it any more
 void require(bool ok) {
   if (!ok) throw NotCommon();
 }
@@ -138,7 +148,12 @@ struct Call {
   }
 };
 
-void done(int rc) { require(rc == HPC_OK); }
+// What the library answered. Everything but HPC_ERR_CUDA is found before the first launch.
+void done(int rc, const char* name) {
+  if (rc == HPC_ERR_CUDA) throw NotLaunched{rc, name};
+  require(rc == HPC_OK);
+  accepted = true;
+}
 
 PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
 
@@ -146,18 +161,29 @@ template <typename... T>
 PyObject* tuple(const T&... t) {
   PyObject* items[] = {t.defined() ? wrap(t) : Py_NewRef(Py_None)...};
   PyObject* r = PyTuple_New(sizeof...(T));
+  if (!r) return nullptr;
   for (size_t i = 0; i < sizeof...(T); ++i) PyTuple_SET_ITEM(r, i, items[i]);
   return r;
 }
 
-// Runs f; None for what is not the common form or fails (the long way then says why).
+// Runs f; None for what is not the common form or fails before the library has it (the long way then says why).
 template <typename F>
 PyObject* run(Py_ssize_t n, Py_ssize_t want, F f) {
   if (n != want) Py_RETURN_NONE;
+  accepted = false;
   try {
     return f();
   } catch (const NotCommon&) {
-  } catch (const std::exception&) {
+  } catch (const NotLaunched& e) {
+    PyObject* r = PyObject_CallFunction(check, "is", e.rc, e.name);
+    if (r) PyErr_SetString(PyExc_RuntimeError, e.name);
+    Py_XDECREF(r);
+    return nullptr;
+  } catch (const std::exception& e) {
+    if (accepted) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+      return nullptr;
+    }
   }
   PyErr_Clear();
   Py_RETURN_NONE;
@@ -202,7 +228,8 @@ PyObject* resize_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     done(api.pages_resize(p.table, i32(table_out), int32(p.rows), int32(p.max_pages), int32(integer(a[4])),
                           static_cast<const int32_t*>(c.in(tensor(a[1]), at::kInt)),
                           static_cast<const int32_t*>(c.in(tensor(a[2]), at::kInt)), p.ref, i32(ref_out),
-                          int32(p.num_pages), i32(moves), int32(moves.size(0)), i32(count), word(status), c.stream));
+                          int32(p.num_pages), i32(moves), int32(moves.size(0)), i32(count), word(status), c.stream),
+         "hpc_pages_resize");
     return tuple(table_out, ref_out, moves, count, status);
   });
 }
@@ -221,7 +248,8 @@ PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     done(api.pages_fork(p.table, static_cast<const int32_t*>(c.in(tensor(a[1]), at::kInt)), int32(p.rows),
                         static_cast<const int32_t*>(c.in(parents, at::kInt)), i32(table_out), i32(lens_out), int32(rows),
                         int32(p.max_pages), int32(integer(a[4])), p.ref, i32(ref_out), int32(p.num_pages), i32(moves),
-                        int32(moves.size(0)), i32(count), word(status), c.stream));
+                        int32(moves.size(0)), i32(count), word(status), c.stream),
+         "hpc_pages_fork");
     return tuple(table_out, ref_out, moves, count, status, lens_out);
   });
 }
@@ -237,7 +265,8 @@ PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  count = c.out(a[6], at::kInt, {1}), status = c.status(a[7]), none;
     done(api.pages_compact(p.table, i32(table_out), int32(p.rows), int32(p.max_pages), p.ref, i32(ref_out),
                            int32(p.num_pages), i32(map), i32(moves), int32(moves.size(0)), i32(count), word(status),
-                           c.stream));
+                           c.stream),
+         "hpc_pages_compact");
     return tuple(table_out, ref_out, moves, count, status, none, map);
   });
 }
@@ -262,7 +291,8 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     done(api.pages_copy(base.data(), static_cast<int32_t>(caches),
                         first.numel() / first.size(0) * static_cast<int64_t>(first.element_size()), int32(first.size(0)),
                         static_cast<const int32_t*>(c.in(moves, at::kInt)), int32(moves.size(0)),
-                        static_cast<const int32_t*>(c.in(count, at::kInt)), word(status), c.stream));
+                        static_cast<const int32_t*>(c.in(count, at::kInt)), word(status), c.stream),
+         "hpc_pages_copy");
     return wrap(status);
   });
 }
@@ -286,7 +316,8 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            type == at::kFloat ? HPC_FP32 : HPC_BF16,
                            static_cast<const float*>(c.in(u, at::kFloat, {B, T + 1})),
                            static_cast<const int32_t*>(c.optional(a[4], at::kInt, B)), lens, int32(B), int32(T), int32(V),
-                           i32(tokens), i32(accepted), lens ? i32(new_lens) : nullptr, word(status), c.stream));
+                           i32(tokens), i32(accepted), lens ? i32(new_lens) : nullptr, word(status), c.stream),
+         "hpc_verify_drafts");
     return tuple(tokens, accepted, new_lens, status);
   });
 }
@@ -352,7 +383,8 @@ PyObject* prompt_prologue(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              static_cast<float>(number(a[15])), q.data_ptr(), k.data_ptr(), cache.k, cache.v,
                              e4m3 ? HPC_E4M3 : HPC_BF16, nhd ? HPC_NHD : HPC_HND, scales[0], scales[1], cache.num_pages,
                              cache.page_size, r.table, r.max_pages, r.lens, int32(Hq), int32(Hkv), int32(D), word(status),
-                             c.stream));
+                             c.stream),
+         "hpc_prompt_prologue");
     return tuple(q, k, status);
   });
 }
@@ -412,7 +444,8 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               static_cast<const int32_t*>(c.in(cu, at::kInt)), cu_k, int32(cu.numel() - 1), int32(q.heads),
                               int32(k.heads), int32(q.D), a[5] == Py_True, scale_of(a[6], q.D), out.data_ptr(),
                               lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
-                              scratch.bytes(), word(status), c.stream));
+                              scratch.bytes(), word(status), c.stream),
+         "hpc_prompt_attention");
     return tuple(out, lse, status);
   });
 }
@@ -435,25 +468,28 @@ PyObject* prompt_attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                     scale_of(a[7], q.D), out.data_ptr(),
                                     lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
                               scratch.bytes(), word(status),
-                                    c.stream));
+                                    c.stream),
+         "hpc_prompt_attention_paged");
     return tuple(out, lse, status);
   });
 }
 
-// bind(addresses): the library's functions, in the order of Api.
+// bind(check, addresses): what raises a library call's error, and the library's functions in the order of Api.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* f[9];
-  if (n != 9) {
-    PyErr_SetString(PyExc_ValueError, "bind takes nine addresses");
+  if (n != 10) {
+    PyErr_SetString(PyExc_ValueError, "bind takes a function and nine addresses");
     return nullptr;
   }
   for (int i = 0; i < 9; ++i) {
-    f[i] = PyLong_AsVoidPtr(a[i]);
+    f[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
       return nullptr;
     }
   }
+  Py_INCREF(a[0]);
+  Py_XSETREF(check, a[0]);
   api = {reinterpret_cast<decltype(api.prompt_prologue)>(f[0]), reinterpret_cast<decltype(api.prompt_attention)>(f[1]),
          reinterpret_cast<decltype(api.prompt_attention_paged)>(f[2]), reinterpret_cast<decltype(api.verify_drafts)>(f[3]),
          reinterpret_cast<decltype(api.pages_resize)>(f[4]), reinterpret_cast<decltype(api.pages_fork)>(f[5]),

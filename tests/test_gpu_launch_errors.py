@@ -59,3 +59,29 @@ def test_an_update_after_a_refused_launch_runs_once(B, monkeypatch, short):
     same(t, want[0])
     same(c, want[1])
     same(up.page_map, want[2])
+
+
+def test_a_launch_that_fails_is_not_tried_again(B, monkeypatch):
+    """The short way with a library whose resize reports a failed launch: the long way must not run it again."""
+    assert B._fast is not None
+    tried = []
+
+    class Library:
+        def __getattr__(self, name):
+            if name.startswith("hpc_pages"):
+                tried.append(name)
+            return getattr(lib, name)
+
+    lib, resize = B._lib, B._lib.hpc_pages_resize
+    fake = ctypes.CFUNCTYPE(ctypes.c_int, *resize.argtypes)(lambda *a: tried.append("short") or B.HPC_ERR_CUDA)
+    at = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in B._FAST_CALLS]
+    at[B._FAST_CALLS.index("hpc_pages_resize")] = ctypes.cast(fake, ctypes.c_void_p).value
+    t, o, n, c = dev(*(np.zeros(s, dtype=np.int32) for s in ((2, 3), 2, 2, 5)))
+    monkeypatch.setattr(B, "_lib", Library())
+    try:
+        B._fast.bind(B._check, *at)
+        with pytest.raises(B.HpcError, match="hpc_pages_resize: CUDA error"):
+            B.resize_pages(t, o, n, c, 16)
+    finally:
+        B._bind(lib)
+    assert tried == ["short"]
