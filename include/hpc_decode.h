@@ -519,8 +519,9 @@ HPC_API int hpc_prompt_prologue(const void* qkv, int64_t tokens, const int32_t* 
  *   head_dim 64 or 128; num_heads / kv_heads in {1, 2, 4, 8}; sm_scale positive and finite.
  * A query that sees no key (m_r < n_r) gets zeros and -inf. A sequence whose lengths do not hold together
  * (descending, or past tokens / kv_tokens) sets HPC_DEV_BAD_SEQLEN and is left out. Values of keys that a
- * query does not see never reach its result, infinities and NaN included. P is rounded to bf16 for its
- * product with V; sums and the softmax are fp32.
+ * query does not see never reach its result, infinities and NaN included (where the values of keys that some of a
+ * CTA's queries see hold some, those queries are done one by one, which takes up to about 20 us per key of the sequence).
+ * P is rounded to bf16 for its product with V; sums and the softmax are fp32.
  *   work:    device uint32 [HPC_PROMPT_WORK_WORDS], zero at every call; left unspecified.
  *   partial: device scratch of partial_bytes, 16-byte aligned, or NULL with 0: where the work of few queries on
  *            many keys can be cut along the keys. hpc_prompt_attention_partial_bytes() is the most it uses;

@@ -47,7 +47,10 @@
 // Roles (384 threads): warps 0-3 softmax of A, 4-7 of B (also the epilogues), warp 8 issues the products with
 // K, warp 10 those with V, warp 9 looks up units and loads, warp 11 checks V. A softmax thread holds the 128
 // scores of its row, so the softmax warpgroups take registers from the third (208 + 208 + 88 = 3 x the 168 of the
-// launch). Every wait is bounded (2 s) and ends in HPC_DEV_TIMEOUT.
+// launch). Every wait is bounded and ends in HPC_DEV_TIMEOUT: by 2 s and 64 us for each key that a sequence can have,
+// since rows that are done one by one (values that are not finite) keep the other roles waiting. 32 rows of a warp took
+// 0.19 to 0.65 us for each key (packed, and pages of 16 with every CTA at it), so that 2 s alone passed at 96000 keys.
+// (Waits that look whether such rows advance kept to 2 s, and cost 2 to 12% of every call.)
 #include <cmath>
 
 #include "umma_bf16.cuh"
@@ -71,6 +74,7 @@ constexpr int kPaMinPart = 6;           // blocks: joining costs more than short
 constexpr int kPaMinSave = 5;           // blocks that cutting has to save
 constexpr int kPaMaxParts = 32;
 constexpr int kPaCuts = 512;            // cut units that the scratch can describe, ahead of the slots
+constexpr uint64_t kPaRowsNs = 64000;   // 32 rows one by one, for each key: three times the slowest seen
 
 template <int D>
 struct PaLayout {
@@ -117,6 +121,7 @@ struct PaArgs {
   PaCut* cuts;
   float* partial;  // [slots][2 tiles][m 128, l 128, O (D / 4) x 128 x 4]
   int64_t tokens, kv_tokens, max_pages;
+  uint64_t limit_ns;  // of a wait
   float scale_log2, scale;
   int32_t batch, Hq, Hkv, group, causal, P, num_pages, nhd, slots;
   int32_t unsorted;  // a CTA for every unit: they are dealt as they come
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   bool ok = true;
   uint32_t err = 0;
   auto wait = [&](uint64_t& b, uint32_t parity) -> bool {
-    if (ok && !mbar_wait(smem_u32(&b), parity)) {
+    if (ok && !mbar_wait(smem_u32(&b), parity, a.limit_ns)) {
       ok = false;
       err = HPC_DEV_TIMEOUT;
     }
@@ -901,7 +906,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       int stage = scores ? 0 : 1;  // ring position of K_j (V_j): stage and phase
       uint32_t phase = 0;
       auto wait_all = [&](uint64_t& b, uint32_t parity) -> bool {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&b), parity));
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&b), parity, a.limit_ns));
         if (!ok) err = HPC_DEV_TIMEOUT;
         return ok;
       };
@@ -1141,6 +1146,7 @@ int pa_common(const void* q, int64_t q_token_stride, int64_t q_head_stride, int6
     a.cuts = static_cast<PaCut*>(partial);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(partial) + kPaCutBytes);
   }
+  a.limit_ns = kWaitLimitNs + (max_keys > 0 ? static_cast<uint64_t>(max_keys) * kPaRowsNs : 0);
   a.tokens = tokens;
   a.scale = sm_scale;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
