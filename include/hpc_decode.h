@@ -565,12 +565,22 @@ HPC_API int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride, in
  *   Caches, scales, block_table, seq_lens as hpc_decode_prologue; any page_size; batch <= 8192.
  * Requests from the first on that does not fit into kv_tokens rows are left out (no rows) and set
  * HPC_DEV_CAPACITY. A length that is negative or beyond the block table counts as 0 and sets
- * HPC_DEV_BAD_SEQLEN; tokens of a page out of range are zeros and set HPC_DEV_BAD_PAGE. */
+ * HPC_DEV_BAD_SEQLEN; tokens of a page out of range are zeros and set HPC_DEV_BAD_PAGE.
+ * hpc_gather_prompt_tokens is the same for prompts, or chunks of them, whose queries are the last of those tokens: a length
+ * below the request's cu_queries[r+1] - cu_queries[r] queries (device int32 [batch + 1]) counts as 0 and sets
+ * HPC_DEV_BAD_SEQLEN too, as in hpc_prompt_attention_paged. hpc_prompt_attention, for which fewer keys than queries are
+ * no error, then gives such a request zeros and -inf. */
 HPC_API int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype, hpc_kv_layout kv_layout,
                               const float* k_scale, const float* v_scale, int32_t num_pages, int32_t page_size,
                               const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
                               int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t kv_tokens, void* k_out,
                               void* v_out, int32_t* cu_seqlens, uint32_t* status, void* stream);
+HPC_API int hpc_gather_prompt_tokens(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype,
+                                     hpc_kv_layout kv_layout, const float* k_scale, const float* v_scale,
+                                     int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                                     int32_t max_pages_per_req, const int32_t* seq_lens, const int32_t* cu_queries,
+                                     int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t kv_tokens, void* k_out,
+                                     void* v_out, int32_t* cu_seqlens, uint32_t* status, void* stream);
 
 /* ---- verification of drafted tokens -----------------------------------------------------
  * After hpc_decode_step_multi has run the target over the drafted tokens: which of them stand, and the

@@ -43,7 +43,7 @@ EXPORTS = ("hpc_step_record_bytes", "hpc_build_flags", "hpc_plan_workspace_bytes
            "hpc_merge_lse", "hpc_wait_selftest", "hpc_merge_lse_gather", "hpc_gather_rows", "hpc_gather_pages",
            "hpc_prompt_prologue", "hpc_verify_drafts", "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact",
            "hpc_pages_copy", "hpc_prompt_attention", "hpc_prompt_attention_paged",
-           "hpc_prompt_attention_partial_bytes", "hpc_gather_tokens")
+           "hpc_prompt_attention_partial_bytes", "hpc_gather_tokens", "hpc_gather_prompt_tokens")
 
 
 class HpcError(RuntimeError):
@@ -129,6 +129,8 @@ def _load(path=LIB):
         "hpc_prompt_attention_partial_bytes": (sz, [i32]),
         "hpc_gather_tokens": (ctypes.c_int, [vp, vp, ctypes.c_int, ctypes.c_int, vp, vp, i32, i32, vp, i32, vp, i32, i32,
                                              i32, i64, vp, vp, vp, vp, vp]),
+        "hpc_gather_prompt_tokens": (ctypes.c_int, [vp, vp, ctypes.c_int, ctypes.c_int, vp, vp, i32, i32, vp, i32, vp, vp,
+                                                    i32, i32, i32, i64, vp, vp, vp, vp, vp]),
         "hpc_prompt_attention_paged": (ctypes.c_int, [vp, i64, i64, vp, vp, ctypes.c_int, ctypes.c_int, i32, i32, vp, i32,
                                                       vp, i64, vp, i32, i32, i32, i32, fp, vp, vp, vp, vp, sz, vp, vp]),
         "hpc_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -898,10 +900,11 @@ def prompt_attention(q, k, v, cu_seqlens, *, cu_seqlens_k=None, causal=True, sm_
 
 
 def gather_tokens(k_pages, v_pages, block_table, seq_lens, kv_tokens, *, kv_dtype="bf16", kv_layout="HND", k_scale=None,
-                  v_scale=None, k_out=None, v_out=None, cu_seqlens=None, status=None):
+                  v_scale=None, k_out=None, v_out=None, cu_seqlens=None, status=None, cu_queries=None):
     """The cached tokens of every request as packed bf16 rows (``hpc_gather_tokens``), kv_tokens rows at most. Returns
     (k, v [kv_tokens, Hkv, D], cu_seqlens int32 [batch + 1], status); rows past cu_seqlens[batch] are left as
-    they were."""
+    they were. With cu_queries, the boundaries of queries that are the last of those tokens, a request with fewer cached
+    tokens than queries is flagged and has no rows (``hpc_gather_prompt_tokens``)."""
     _need(k_pages, "k_pages")
     dev, D = k_pages.device, k_pages.shape[-1]
     code, num_pages, Hkv, P, lay = _cache(k_pages, v_pages, kv_dtype, kv_layout, k_scale, v_scale, D, dev)
@@ -913,10 +916,15 @@ def gather_tokens(k_pages, v_pages, block_table, seq_lens, kv_tokens, *, kv_dtyp
     k_out = _buffer(k_out, "k_out", (int(kv_tokens), Hkv, D), torch.bfloat16, dev)
     v_out = _buffer(v_out, "v_out", (int(kv_tokens), Hkv, D), torch.bfloat16, dev)
     cu_seqlens = _buffer(cu_seqlens, "cu_seqlens", (batch + 1,), torch.int32, dev)
+    queries = ()
+    if cu_queries is not None:
+        _packed(cu_queries, dev, batch)
+        queries = (cu_queries.data_ptr(),)
     status = _status(status, dev)
-    _launch("hpc_gather_tokens", dev, k_pages.data_ptr(), v_pages.data_ptr(), code, lay, _addr(k_scale), _addr(v_scale),
-            num_pages, P, block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), batch, Hkv, D, int(kv_tokens),
-            k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), status.data_ptr())
+    _launch("hpc_gather_prompt_tokens" if queries else "hpc_gather_tokens", dev, k_pages.data_ptr(), v_pages.data_ptr(), code,
+            lay, _addr(k_scale), _addr(v_scale), num_pages, P, block_table.data_ptr(), block_table.shape[1],
+            seq_lens.data_ptr(), *queries, batch, Hkv, D, int(kv_tokens), k_out.data_ptr(), v_out.data_ptr(),
+            cu_seqlens.data_ptr(), status.data_ptr())
     return k_out, v_out, cu_seqlens, status
 
 
@@ -929,12 +937,14 @@ def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlen
 
     The kernel reads bf16 pages of 16, 32, 64 or 128 tokens. With kv_tokens, an upper bound of the sum of seq_lens
     (which is on the device), the cached tokens are read into packed rows first (``gather_tokens``): for E4M3 caches,
-    which need it, and pages of any size."""
+    which need it, and pages of any size. A request that is flagged for its length, which the kernel leaves alone, gets
+    zeros and -inf this way, and so does one that kv_tokens leaves out."""
     if kv_tokens is None and kv_dtype != "bf16":
         raise HpcError(f"prompt_attention_paged of a {kv_dtype} cache needs kv_tokens, a bound of the sum of seq_lens")
     if kv_tokens is not None:
         k, v, cu_k, status = gather_tokens(k_pages, v_pages, block_table, seq_lens, kv_tokens, kv_dtype=kv_dtype,
-                                           kv_layout=kv_layout, k_scale=k_scale, v_scale=v_scale, status=status)
+                                           kv_layout=kv_layout, k_scale=k_scale, v_scale=v_scale, status=status,
+                                           cu_queries=cu_seqlens)
         return prompt_attention(q, k, v, cu_seqlens, cu_seqlens_k=cu_k, sm_scale=sm_scale, out=out, lse=lse,
                                 return_lse=return_lse, status=status)
     if _fast is not None:

@@ -24,6 +24,7 @@ struct GtArgs {
   const void *k_pages, *v_pages;
   const float *k_scale, *v_scale;
   const int32_t *table, *seq_lens;
+  const int32_t* cu_q;  // or null: no queries to count
   __nv_bfloat16 *k, *v;
   int32_t* cu;
   uint32_t* status;
@@ -63,7 +64,8 @@ __global__ void __launch_bounds__(kGtThreads, kGtCtas) gather_tokens_kernel(cons
   for (int32_t r0 = 0; r0 < a.batch; r0 += kGtThreads) {
     const int32_t r = r0 + static_cast<int32_t>(threadIdx.x);
     int32_t n = r < a.batch ? a.seq_lens[r] : 0;
-    const bool bad = n < 0 || static_cast<int64_t>(n) > a.max_pages * a.P;
+    bool bad = n < 0 || static_cast<int64_t>(n) > a.max_pages * a.P;
+    if (a.cu_q && r < a.batch) bad |= static_cast<int64_t>(a.cu_q[r + 1]) - a.cu_q[r] > n;
     if (bad) n = 0;
     int32_t x = n;
 #pragma unroll
@@ -130,16 +132,11 @@ __global__ void __launch_bounds__(kGtThreads, kGtCtas) gather_tokens_kernel(cons
   }
 }
 
-}  // namespace
-}  // namespace hpc
-
-using namespace hpc;
-
-extern "C" int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype, hpc_kv_layout kv_layout,
-                                 const float* k_scale, const float* v_scale, int32_t num_pages, int32_t page_size,
-                                 const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
-                                 int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t kv_tokens, void* k_out,
-                                 void* v_out, int32_t* cu_seqlens, uint32_t* status, void* stream) {
+int gather(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype, hpc_kv_layout kv_layout, const float* k_scale,
+           const float* v_scale, int32_t num_pages, int32_t page_size, const int32_t* block_table,
+           int32_t max_pages_per_req, const int32_t* seq_lens, const int32_t* cu_queries, int32_t batch, int32_t kv_heads,
+           int32_t head_dim, int64_t kv_tokens, void* k_out, void* v_out, int32_t* cu_seqlens, uint32_t* status,
+           void* stream) {
   if (kv_tokens < 0 || kv_tokens > INT32_MAX - 1024) return fail(HPC_ERR_ARG, "kv_tokens out of range");
   if (!k_pages || !v_pages || !block_table || !seq_lens || !cu_seqlens || !status || (kv_tokens > 0 && (!k_out || !v_out)))
     return fail(HPC_ERR_ARG, "null pointer argument");
@@ -161,6 +158,7 @@ extern "C" int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_d
   a.v_scale = v_scale;
   a.table = block_table;
   a.seq_lens = seq_lens;
+  a.cu_q = cu_queries;
   a.k = static_cast<__nv_bfloat16*>(k_out);
   a.v = static_cast<__nv_bfloat16*>(v_out);
   a.cu = cu_seqlens;
@@ -181,4 +179,31 @@ extern "C" int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_d
   const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kGtThreads),
                                    (static_cast<size_t>(batch) + 1) * 4, static_cast<cudaStream_t>(stream), a);
   return launched(e, "gather_tokens_kernel");
+}
+
+}  // namespace
+}  // namespace hpc
+
+using namespace hpc;
+
+extern "C" int hpc_gather_tokens(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype, hpc_kv_layout kv_layout,
+                                 const float* k_scale, const float* v_scale, int32_t num_pages, int32_t page_size,
+                                 const int32_t* block_table, int32_t max_pages_per_req, const int32_t* seq_lens,
+                                 int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t kv_tokens, void* k_out,
+                                 void* v_out, int32_t* cu_seqlens, uint32_t* status, void* stream) {
+  return gather(k_pages, v_pages, kv_dtype, kv_layout, k_scale, v_scale, num_pages, page_size, block_table,
+                max_pages_per_req, seq_lens, nullptr, batch, kv_heads, head_dim, kv_tokens, k_out, v_out, cu_seqlens,
+                status, stream);
+}
+
+extern "C" int hpc_gather_prompt_tokens(const void* k_pages, const void* v_pages, hpc_dtype kv_dtype,
+                                        hpc_kv_layout kv_layout, const float* k_scale, const float* v_scale,
+                                        int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                                        int32_t max_pages_per_req, const int32_t* seq_lens, const int32_t* cu_queries,
+                                        int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t kv_tokens, void* k_out,
+                                        void* v_out, int32_t* cu_seqlens, uint32_t* status, void* stream) {
+  if (!cu_queries) return fail(HPC_ERR_ARG, "null pointer argument");
+  return gather(k_pages, v_pages, kv_dtype, kv_layout, k_scale, v_scale, num_pages, page_size, block_table,
+                max_pages_per_req, seq_lens, cu_queries, batch, kv_heads, head_dim, kv_tokens, k_out, v_out, cu_seqlens,
+                status, stream);
 }
