@@ -147,6 +147,7 @@ try:  # the short way in for calls in the common form; without it every call goe
     from . import _fastcall as _fast
 except ImportError:
     _fast = None
+_status_word = None if _fast is None else _fast.status_word
 _FAST_CALLS = ("hpc_prompt_prologue", "hpc_prompt_attention", "hpc_prompt_attention_paged", "hpc_verify_drafts",
                "hpc_pages_resize", "hpc_pages_fork", "hpc_pages_compact", "hpc_pages_copy",
                "hpc_prompt_attention_partial_bytes")
@@ -759,24 +760,15 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-_words = {}  # (device, stream) -> status words zeroed there and not handed out yet
-
-
 def _status(status, dev):
-    """The caller's status word, or a zeroed one. Words are zeroed 128 at a time on the stream that will use
-    them: a memset of its own for each call costs as much as a small kernel. A captured call zeroes its
-    own word, at every replay."""
+    """The caller's status word, or a zeroed one: one of those that the short way zeroes 128 at a time, since a memset
+    of its own for each call costs as much as a small kernel. A captured call zeroes its own word, at every
+    replay."""
     if status is not None:
         _want(status, "status", torch.int32, dev)
         return status
-    if torch.cuda.is_current_stream_capturing():
-        return new_status(dev)
-    words = _words.setdefault((dev.index, torch._C._cuda_getCurrentRawStream(dev.index)), [])
-    try:
-        return words.pop()
-    except IndexError:
-        words.extend(torch.zeros(128, dtype=torch.int32, device=dev).split(1))
-        return words.pop()
+    word = None if _status_word is None else _status_word(dev.index)
+    return new_status(dev) if word is None else word
 
 
 def _launch(name, dev, *args):

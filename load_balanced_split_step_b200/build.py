@@ -84,7 +84,8 @@ def build_fastcall(force: bool = False) -> str:
     libs = cpp_extension.library_paths()
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-DUSE_CUDA",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in dirs), src, "-o",
-           FASTCALL + ".tmp", *(f"-L{d}" for d in libs), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+           FASTCALL + ".tmp", *(f"-L{d}" for d in libs), f"-L{os.path.join(cuda, 'lib64')}", "-lcudart", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     if proc.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + proc.stdout + proc.stderr)

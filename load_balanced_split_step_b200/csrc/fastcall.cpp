@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -92,12 +93,11 @@ struct Call {
   c10::DeviceIndex dev;
   void* stream;
 
-  explicit Call(const Tensor& first) {
-    require(first.is_cuda());
-    dev = first.get_device();
-    require(c10::cuda::current_device() == dev);
+  explicit Call(int64_t device) : dev(static_cast<c10::DeviceIndex>(device)) {
+    require(c10::cuda::current_device() == device);
     stream = c10::cuda::getCurrentCUDAStream(dev).stream();
   }
+  explicit Call(const Tensor& first) : Call(first.is_cuda() ? first.get_device() : -1) {}
 
   // A contiguous tensor of this device and type.
   void* in(const Tensor& t, ScalarType type) const {
@@ -133,15 +133,26 @@ struct Call {
     return zeroed<1, 128>();
   }
   // kWords zeroed words that nothing else has had: kTimes of them are zeroed at a time on the stream that uses
-  // them, since a memset of its own for each call costs as much as a small kernel.
+  // them, since a memset of its own for each call costs as much as a small kernel. Later calls get the others, so
+  // they are plain tensors whatever mode this call runs in (inference, a dispatch mode): made without the dispatcher,
+  // and not views of one another.
   template <int64_t kWords, int64_t kTimes>
   Tensor zeroed() const {
     require(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None);
     static auto* pieces = new std::unordered_map<void*, std::vector<Tensor>>[64];  // never freed: the driver may be gone
     require(dev < 64);
     std::vector<Tensor>& left = pieces[dev][stream];
-    if (left.empty())
-      left = at::zeros({kWords * kTimes}, at::TensorOptions().dtype(at::kInt).device(c10::Device(c10::kCUDA, dev))).split(kWords);
+    if (left.empty()) {
+      const c10::InferenceMode normal(false);
+      const Tensor all = out(Py_None, at::kInt, {kWords * kTimes});
+      require(cudaMemsetAsync(all.data_ptr(), 0, all.nbytes(), static_cast<cudaStream_t>(stream)) == cudaSuccess);
+      for (int64_t i = 0; i < kTimes; ++i) {
+        auto piece = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        piece->set_sizes_contiguous({kWords});
+        piece->set_storage_offset(i * kWords);
+        left.emplace_back(std::move(piece));
+      }
+    }
     Tensor t = std::move(left.back());
     left.pop_back();
     return t;
@@ -191,6 +202,14 @@ PyObject* run(Py_ssize_t n, Py_ssize_t want, F f) {
 
 int32_t* i32(const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
 uint32_t* word(const Tensor& t) { return reinterpret_cast<uint32_t*>(t.data_ptr()); }
+
+// device index: a zeroed status word for a call on that device's current stream.
+PyObject* status_word(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 1, [&] {
+    const Call c(integer(a[0]));
+    return wrap(c.status(Py_None));
+  });
+}
 
 // ---- pages
 struct Pool {
@@ -502,6 +521,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {ENTRY(bind),          ENTRY(resize_pages),    ENTRY(fork_pages),
                          ENTRY(compact_pages), ENTRY(copy_pages),      ENTRY(verify_drafts),
                          ENTRY(prompt_prologue), ENTRY(prompt_attention), ENTRY(prompt_attention_paged),
+                         ENTRY(status_word),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
