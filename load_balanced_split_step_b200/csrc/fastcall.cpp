@@ -51,7 +51,7 @@ struct NotLaunched {
   int rc;
   const char* name;
 };
-bool accepted = false;  // the library has taken this call: there is no other way for it any more
+thread_local bool accepted = false;  // the library has taken this call: there is no other way for it any more
 void require(bool ok) {
   if (!ok) throw NotCommon();
 }
@@ -87,6 +87,14 @@ double number(PyObject* o) {
   }
   return v;
 }
+
+// Other Python threads run meanwhile: a launch waits while the stream's queue is full.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 // One call: the device of its first tensor, its stream, and its outputs.
 struct Call {
@@ -145,7 +153,10 @@ struct Call {
     if (left.empty()) {
       const c10::InferenceMode normal(false);
       const Tensor all = out(Py_None, at::kInt, {kWords * kTimes});
-      require(cudaMemsetAsync(all.data_ptr(), 0, all.nbytes(), static_cast<cudaStream_t>(stream)) == cudaSuccess);
+      {
+        const Unlocked unlocked;
+        require(cudaMemsetAsync(all.data_ptr(), 0, all.nbytes(), static_cast<cudaStream_t>(stream)) == cudaSuccess);
+      }
       for (int64_t i = 0; i < kTimes; ++i) {
         auto piece = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
         piece->set_sizes_contiguous({kWords});
@@ -159,8 +170,14 @@ struct Call {
   }
 };
 
-// What the library answered. Everything but HPC_ERR_CUDA is found before the first launch.
-void done(int rc, const char* name) {
+// Calls the library. Everything but HPC_ERR_CUDA is found before the first launch.
+template <typename... P, typename... A>
+void launch(const char* name, int (*f)(P...), A... args) {
+  int rc;
+  {
+    const Unlocked unlocked;
+    rc = f(args...);
+  }
   if (rc == HPC_ERR_CUDA) throw NotLaunched{rc, name};
   require(rc == HPC_OK);
   accepted = true;
@@ -244,11 +261,10 @@ PyObject* resize_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     require(tensor(a[1]).numel() == p.rows && tensor(a[2]).numel() == p.rows);
     const Tensor table_out = c.out(a[5], at::kInt, {p.rows, p.max_pages}), ref_out = c.out(a[6], at::kInt, {p.num_pages}),
                  moves = moves_out(c, a[7], p.rows), count = c.out(a[8], at::kInt, {1}), status = c.status(a[9]);
-    done(api.pages_resize(p.table, i32(table_out), int32(p.rows), int32(p.max_pages), int32(integer(a[4])),
-                          static_cast<const int32_t*>(c.in(tensor(a[1]), at::kInt)),
-                          static_cast<const int32_t*>(c.in(tensor(a[2]), at::kInt)), p.ref, i32(ref_out),
-                          int32(p.num_pages), i32(moves), int32(moves.size(0)), i32(count), word(status), c.stream),
-         "hpc_pages_resize");
+    launch("hpc_pages_resize", api.pages_resize, p.table, i32(table_out), int32(p.rows), int32(p.max_pages),
+           int32(integer(a[4])), static_cast<const int32_t*>(c.in(tensor(a[1]), at::kInt)),
+           static_cast<const int32_t*>(c.in(tensor(a[2]), at::kInt)), p.ref, i32(ref_out), int32(p.num_pages),
+           i32(moves), int32(moves.size(0)), i32(count), word(status), c.stream);
     return tuple(table_out, ref_out, moves, count, status);
   });
 }
@@ -264,11 +280,10 @@ PyObject* fork_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor table_out = c.out(a[5], at::kInt, {rows, p.max_pages}), lens_out = c.out(a[6], at::kInt, {rows}),
                  ref_out = c.out(a[7], at::kInt, {p.num_pages}), moves = moves_out(c, a[8], rows),
                  count = c.out(a[9], at::kInt, {1}), status = c.status(a[10]);
-    done(api.pages_fork(p.table, static_cast<const int32_t*>(c.in(tensor(a[1]), at::kInt)), int32(p.rows),
-                        static_cast<const int32_t*>(c.in(parents, at::kInt)), i32(table_out), i32(lens_out), int32(rows),
-                        int32(p.max_pages), int32(integer(a[4])), p.ref, i32(ref_out), int32(p.num_pages), i32(moves),
-                        int32(moves.size(0)), i32(count), word(status), c.stream),
-         "hpc_pages_fork");
+    launch("hpc_pages_fork", api.pages_fork, p.table, static_cast<const int32_t*>(c.in(tensor(a[1]), at::kInt)),
+           int32(p.rows), static_cast<const int32_t*>(c.in(parents, at::kInt)), i32(table_out), i32(lens_out),
+           int32(rows), int32(p.max_pages), int32(integer(a[4])), p.ref, i32(ref_out), int32(p.num_pages), i32(moves),
+           int32(moves.size(0)), i32(count), word(status), c.stream);
     return tuple(table_out, ref_out, moves, count, status, lens_out);
   });
 }
@@ -282,10 +297,9 @@ PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor table_out = c.out(a[2], at::kInt, {p.rows, p.max_pages}), ref_out = c.out(a[3], at::kInt, {p.num_pages}),
                  map = c.out(a[4], at::kInt, {p.num_pages}), moves = moves_out(c, a[5], p.num_pages / 2),
                  count = c.out(a[6], at::kInt, {1}), status = c.status(a[7]), none;
-    done(api.pages_compact(p.table, i32(table_out), int32(p.rows), int32(p.max_pages), p.ref, i32(ref_out),
-                           int32(p.num_pages), i32(map), i32(moves), int32(moves.size(0)), i32(count), word(status),
-                           c.stream),
-         "hpc_pages_compact");
+    launch("hpc_pages_compact", api.pages_compact, p.table, i32(table_out), int32(p.rows), int32(p.max_pages), p.ref,
+           i32(ref_out), int32(p.num_pages), i32(map), i32(moves), int32(moves.size(0)), i32(count), word(status),
+           c.stream);
     return tuple(table_out, ref_out, moves, count, status, none, map);
   });
 }
@@ -307,11 +321,10 @@ PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
       base[i] = c.in(t, t.scalar_type(), first.sizes());
     }
     const Tensor status = c.status(a[3]);
-    done(api.pages_copy(base.data(), static_cast<int32_t>(caches),
-                        first.numel() / first.size(0) * static_cast<int64_t>(first.element_size()), int32(first.size(0)),
-                        static_cast<const int32_t*>(c.in(moves, at::kInt)), int32(moves.size(0)),
-                        static_cast<const int32_t*>(c.in(count, at::kInt)), word(status), c.stream),
-         "hpc_pages_copy");
+    launch("hpc_pages_copy", api.pages_copy, base.data(), static_cast<int32_t>(caches),
+           first.numel() / first.size(0) * static_cast<int64_t>(first.element_size()), int32(first.size(0)),
+           static_cast<const int32_t*>(c.in(moves, at::kInt)), int32(moves.size(0)),
+           static_cast<const int32_t*>(c.in(count, at::kInt)), word(status), c.stream);
     return wrap(status);
   });
 }
@@ -331,12 +344,11 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n) {
     require(lens || !given(a[8]));
     const Tensor tokens = c.out(a[6], at::kInt, {B, T + 1}), accepted = c.out(a[7], at::kInt, {B}),
                  new_lens = lens ? c.out(a[8], at::kInt, {B}) : Tensor(), status = c.status(a[9]);
-    done(api.verify_drafts(static_cast<const int32_t*>(c.in(drafts, at::kInt)), c.in(p, type, {B, T + 1, V}), V, q, V,
-                           type == at::kFloat ? HPC_FP32 : HPC_BF16,
-                           static_cast<const float*>(c.in(u, at::kFloat, {B, T + 1})),
-                           static_cast<const int32_t*>(c.optional(a[4], at::kInt, B)), lens, int32(B), int32(T), int32(V),
-                           i32(tokens), i32(accepted), lens ? i32(new_lens) : nullptr, word(status), c.stream),
-         "hpc_verify_drafts");
+    launch("hpc_verify_drafts", api.verify_drafts, static_cast<const int32_t*>(c.in(drafts, at::kInt)),
+           c.in(p, type, {B, T + 1, V}), V, q, V, type == at::kFloat ? HPC_FP32 : HPC_BF16,
+           static_cast<const float*>(c.in(u, at::kFloat, {B, T + 1})),
+           static_cast<const int32_t*>(c.optional(a[4], at::kInt, B)), lens, int32(B), int32(T), int32(V), i32(tokens),
+           i32(accepted), lens ? i32(new_lens) : nullptr, word(status), c.stream);
     return tuple(tokens, accepted, new_lens, status);
   });
 }
@@ -396,14 +408,12 @@ PyObject* prompt_prologue(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     const Tensor q = c.out(a[16], at::kBFloat16, {tokens, Hq, D}), k = c.out(a[17], at::kBFloat16, {tokens, Hkv, D}),
                  status = c.status(a[18]);
-    done(api.prompt_prologue(c.in(qkv, at::kBFloat16), tokens, r.cu, r.batch,
-                             static_cast<const float*>(c.in(tensor(a[2]), at::kFloat)),
-                             static_cast<const float*>(c.in(tensor(a[3]), at::kFloat)), static_cast<float>(number(a[14])),
-                             static_cast<float>(number(a[15])), q.data_ptr(), k.data_ptr(), cache.k, cache.v,
-                             e4m3 ? HPC_E4M3 : HPC_BF16, nhd ? HPC_NHD : HPC_HND, scales[0], scales[1], cache.num_pages,
-                             cache.page_size, r.table, r.max_pages, r.lens, int32(Hq), int32(Hkv), int32(D), word(status),
-                             c.stream),
-         "hpc_prompt_prologue");
+    launch("hpc_prompt_prologue", api.prompt_prologue, c.in(qkv, at::kBFloat16), tokens, r.cu, r.batch,
+           static_cast<const float*>(c.in(tensor(a[2]), at::kFloat)),
+           static_cast<const float*>(c.in(tensor(a[3]), at::kFloat)), static_cast<float>(number(a[14])),
+           static_cast<float>(number(a[15])), q.data_ptr(), k.data_ptr(), cache.k, cache.v, e4m3 ? HPC_E4M3 : HPC_BF16,
+           nhd ? HPC_NHD : HPC_HND, scales[0], scales[1], cache.num_pages, cache.page_size, r.table, r.max_pages,
+           r.lens, int32(Hq), int32(Hkv), int32(D), word(status), c.stream);
     return tuple(q, k, status);
   });
 }
@@ -458,13 +468,12 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor out = c.out(a[7], at::kBFloat16, {q.tokens, q.heads, q.D}), lse = lse_out(c, a[8], a[9], q),
                  status = c.status(a[10]);
     const Scratch scratch(c, k.tokens, q.D);
-    done(api.prompt_attention(q.at, q.token_stride, q.head_stride, k.at, k.token_stride, k.head_stride, v.at,
-                              v.token_stride, v.head_stride, q.tokens, k.tokens,
-                              static_cast<const int32_t*>(c.in(cu, at::kInt)), cu_k, int32(cu.numel() - 1), int32(q.heads),
-                              int32(k.heads), int32(q.D), a[5] == Py_True, scale_of(a[6], q.D), out.data_ptr(),
-                              lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
-                              scratch.bytes(), word(status), c.stream),
-         "hpc_prompt_attention");
+    launch("hpc_prompt_attention", api.prompt_attention, q.at, q.token_stride, q.head_stride, k.at, k.token_stride,
+           k.head_stride, v.at, v.token_stride, v.head_stride, q.tokens, k.tokens,
+           static_cast<const int32_t*>(c.in(cu, at::kInt)), cu_k, int32(cu.numel() - 1), int32(q.heads),
+           int32(k.heads), int32(q.D), a[5] == Py_True, scale_of(a[6], q.D), out.data_ptr(),
+           lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
+           scratch.bytes(), word(status), c.stream);
     return tuple(out, lse, status);
   });
 }
@@ -481,14 +490,11 @@ PyObject* prompt_attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor out = c.out(a[8], at::kBFloat16, {q.tokens, q.heads, q.D}), lse = lse_out(c, a[9], a[10], q),
                  status = c.status(a[11]);
     const Scratch scratch(c, static_cast<int64_t>(r.max_pages) * cache.page_size, q.D);
-    done(api.prompt_attention_paged(q.at, q.token_stride, q.head_stride, cache.k, cache.v, HPC_BF16,
-                                    nhd ? HPC_NHD : HPC_HND, cache.num_pages, cache.page_size, r.table, r.max_pages,
-                                    r.lens, q.tokens, r.cu, r.batch, int32(q.heads), cache.kv_heads, int32(q.D),
-                                    scale_of(a[7], q.D), out.data_ptr(),
-                                    lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
-                              scratch.bytes(), word(status),
-                                    c.stream),
-         "hpc_prompt_attention_paged");
+    launch("hpc_prompt_attention_paged", api.prompt_attention_paged, q.at, q.token_stride, q.head_stride, cache.k,
+           cache.v, HPC_BF16, nhd ? HPC_NHD : HPC_HND, cache.num_pages, cache.page_size, r.table, r.max_pages, r.lens,
+           q.tokens, r.cu, r.batch, int32(q.heads), cache.kv_heads, int32(q.D), scale_of(a[7], q.D), out.data_ptr(),
+           lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, word(scratch.work), scratch.at(),
+           scratch.bytes(), word(status), c.stream);
     return tuple(out, lse, status);
   });
 }
