@@ -559,7 +559,8 @@ HPC_API int hpc_prompt_attention_paged(const void* q, int64_t q_token_stride, in
 /* The cached tokens of every request as packed bf16 rows, for what reads packed keys: prompt attention over an
  * E4M3 cache or over pages of a size of its own (hpc_prompt_attention with cu_seqlens as cu_seqlens_k).
  *   k_out, v_out: device bf16 [kv_tokens][kv_heads][head_dim], 16-byte aligned: request r's tokens are rows
- *               [cu_seqlens[r], cu_seqlens[r+1]), E4M3 values times their scale, rounded to bf16. Rows past
+ *               [cu_seqlens[r], cu_seqlens[r+1]), E4M3 values times their scale, rounded to bf16 (by 2^-8 of the
+ *               value at most; the decode steps use the codes as they are). Rows past
  *               cu_seqlens[batch] are left as they were.
  *   cu_seqlens: device int32 [batch + 1], written: the prefix sums of the lengths.
  *   Caches, scales, block_table, seq_lens as hpc_decode_prologue; any page_size; batch <= 8192.

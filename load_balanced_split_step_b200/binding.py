@@ -929,7 +929,8 @@ def prompt_attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlen
 
     The kernel reads bf16 pages of 16, 32, 64 or 128 tokens. With kv_tokens, an upper bound of the sum of seq_lens
     (which is on the device), the cached tokens are read into packed rows first (``gather_tokens``): for E4M3 caches,
-    which need it, and pages of any size. A request that is flagged for its length, which the kernel leaves alone, gets
+    which need it, and pages of any size. The rows are bf16: an E4M3 code times its scale is rounded (by 2^-8 of the value at
+    most), where the decode steps use the codes as they are. A request that is flagged for its length, which the kernel leaves alone, gets
     zeros and -inf this way, and so does one that kv_tokens leaves out."""
     if kv_tokens is None and kv_dtype != "bf16":
         raise HpcError(f"prompt_attention_paged of a {kv_dtype} cache needs kv_tokens, a bound of the sum of seq_lens")

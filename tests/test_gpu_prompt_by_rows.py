@@ -1,4 +1,11 @@
-"""Prompt attention over cached tokens by way of packed rows: what it answers to lengths that do not hold together."""
+"""Prompt attention over cached tokens by way of packed rows: what it answers to lengths that do not hold together, and how
+far an E4M3 cache's values are from those that its codes and scales stand for.
+
+Tolerance of the latter. A row's value is code x scale rounded to bf16: off by 2^-8 and 2^-23 (the product in fp32) relative, K
+and V alike. That moves a score by at most S = (2^-8 + 2^-23) sm_scale max_j sum_d |q_d k_jd|, and the sums of the kernel by E
+(as in test_gpu_prompt_attention), so that a normalised weight changes by a factor within exp(+-2 (S + E)); it is rounded to
+bf16 too. With A = sum_j p_j |v_j|: |err| <= A (exp(2 (S + E)) (1 + 2^-8 + 2^-20)^2 - 1), and half a bf16 step of the
+result."""
 import ctypes
 import math
 
@@ -6,7 +13,7 @@ import pytest
 import torch
 
 from tests.test_gpu_gather_tokens import cache
-from tests.test_gpu_prompt_attention import cu, draw
+from tests.test_gpu_prompt_attention import cu, draw, reference
 
 
 @pytest.fixture(scope="module")
@@ -48,6 +55,34 @@ def test_fewer_cached_tokens_than_queries(B, kv, short):
     if 0 <= short < 40:
         _, _, boundaries, st = B.gather_tokens(kp, vp, table, seq, 330, **kw)
         assert int(st.item()) == 0 and boundaries.tolist() == cu((200, short, 90)).tolist()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout,D", [("NHD", 128), ("HND", 64)])
+def test_against_the_values_of_the_cache(B, layout, D):
+    lens, total, Hq, Hkv, P = (1, 130, 7, 300), (1, 130, 1007, 2300), 8, 2, 16
+    (kp, vp), table, seq, _, _ = cache(P, total, Hkv, D, P, layout, "bf16")
+    scale = torch.tensor([0.021, 0.0537], device="cuda")
+    shape = (-1, 1, 1) if layout == "HND" else (-1, 1)
+    kp, vp = [(x.float() / scale.view(shape)).to(torch.float8_e4m3fn) for x in (kp, vp)]
+    q = draw(3, sum(lens), Hq, D)
+    out, lse, st = B.prompt_attention_paged(q, kp, vp, table, seq, cu(lens), return_lse=True, kv_tokens=sum(total),
+                                            kv_dtype="e4m3", kv_layout=layout, k_scale=scale, v_scale=scale)
+    assert int(st.item()) == 0
+    k, v = [x.double() * scale.double().view(shape) for x in (kp, vp)]  # what the codes stand for
+    if layout == "HND":
+        k, v = k.transpose(1, 2), v.transpose(1, 2)
+    o = 0
+    for r, (n, m) in enumerate(zip(lens, total)):
+        pages = table[r, :-(-m // P)].long()
+        want, ls, A, E = reference(q[o:o + n], k[pages].flatten(0, 1)[:m], v[pages].flatten(0, 1)[:m], D ** -0.5, True)
+        moved = E / (D * 2.0 ** -24) * (2.0 ** -8 + 2.0 ** -23) + E
+        tol = A * (torch.exp(2 * moved)[..., None] * (1 + 2.0 ** -8 + 2.0 ** -20) ** 2 - 1)
+        tol = tol + (want.abs() + tol) * 2.0 ** -8
+        err = (out[o:o + n].double() - want).abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
+        assert bool(((lse[o:o + n].double() - ls).abs() <= moved + 2.0 ** -20 * (1 + ls.abs())).all())
+        o += n
 
 
 @pytest.mark.gpu
