@@ -19,8 +19,8 @@
 // source is live, so no page is both.
 //
 // The planners are bound by latency (about eight dependent accesses and three to four barriers) and, in large pools, by
-// what eight SMs copy: a resize of 256 requests in a pool of 40000 pages takes 11.5 us, of 4 requests in one of 512
-// 5.7 us; forks 13.7 and 7.2 us. Each warp reads its run of counts once and keeps it as bits; lengths and
+// what eight SMs copy, about half each: a resize of 256 requests in a pool of 40000 pages takes 11.5 us, of 4 requests
+// in one of 512 5.7 us; forks 13.7 and 7.2 us. Each warp reads its run of counts once and keeps it as bits; lengths and
 // entries that later phases want are loaded under the copy of the counts; divisions are 32-bit (12.9 and 6.6 us without
 // the three).
 #include "hpc_common.cuh"

@@ -18,7 +18,7 @@
 //
 // m_i moves only when a block's maximum exceeds it by more than 8 (log2 units): p stays below 2^8, sums
 // and O are fp32, and the rescaling of O in tensor memory becomes rare. P is rounded to bf16 for its
-// product (relative error 2^-9 per weight, which the output's own bf16 rounding matches); the sum l_i is
+// product (relative error 2^-8 per weight at most, which the output's own bf16 rounding matches); the sum l_i is
 // taken over the unrounded values.
 //
 // Persistent CTAs (one per SM) take units longest first from a counter: units are put in 64 buckets by the number
@@ -29,12 +29,12 @@
 // Where a bucket's units are longer than a CTA's share of all blocks (few heads, or a few new tokens on a long
 // cache), they are cut into parts of about that share; parts leave (m, l, O) in the caller's scratch, and a second
 // kernel, launched behind this one, joins them (a last part that joined the others by itself took 40 us for 18 parts
-// of a tile: one SM reads too little at a time). 16 new tokens of 64/8 heads on 30000 cached ones: 285 us uncut,
-// 41 us so. A part has 6 blocks at least: of 2, 3, 4, 6 and 9
-// that loses least over nine shapes (mixed lengths on 9000 keys 53 us at 2, 47 at 6, 41 at 9; 800 on 1800 keys 22, 25, 29).
-// Cutting has to save 5 blocks, and where it makes up to a third more parts than CTAs, the parts are made longer instead
-// (1700 tokens of 16/8 heads 46.8 us without the two, 39.1 with; 900 on 2400 keys 51.9 and 45.8; the worst of twenty
-// shapes 23.9 and 25.6; all with half the CTAs that join now).
+// of a tile: one SM reads too little at a time). 16 new tokens of 64/8 heads on 30000 keys: 285 us uncut, 40 us so.
+// The rule of the cuts, and what each of its numbers is for, by the times of 22 shapes without it: a part has 6
+// blocks at least (9: half of the shapes 8 to 30% slower; 2 and 4 are as fast, and 10 to 20% faster for up to 200 queries on
+// 1600 keys); a unit up to 1.3 times the share stays whole (16 x 1 on 4000 keys of 32/8 heads 54 us, 66 without); cutting
+// has to save 5 blocks (1700 tokens of 16/8 heads 34 us, 38; but 2518 of 4/2 30.5, 27.9); where it makes up to a third
+// more parts than CTAs, the parts are made longer (900 on 2400 keys of 16/2 heads 38 us, 43).
 // The producer warp looks the units up, ahead of the others, and loads Q and a ring of K and V blocks by TMA
 // (swizzled planes of 64 elements). The next unit's Q has to wait for its place, and comes as far as L2 meanwhile
 // (its arrival after that took 3000 cycles, now 1400).
@@ -383,28 +383,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // buckets that are cut come first, so that a part's number is its place.
         const float share = static_cast<float>(sh.blocks) * a.Hkv / gridDim.x;  // the same in every CTA
         int32_t length = share > kPaMinPart ? static_cast<int32_t>(fminf(ceilf(share), 1e9f)) : kPaMinPart;
-      auto cut = [&](int b) -> int32_t {
-        const int64_t most = (((static_cast<int64_t>(b + 1) << bucket) + 1) << unit_shift) / kPaKeys + 1,
-                      least = ((static_cast<int64_t>(b) << bucket) << unit_shift) / kPaKeys;
-        // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
-        if (10 * most <= 13ll * length || most < length + kPaMinSave || 2 * least < length) return 1;
-        const float n = ceilf(static_cast<float>(most) / static_cast<float>(length));
-        return n < kPaMaxParts ? static_cast<int32_t>(n) : kPaMaxParts;
-      };
-      const int32_t room = a.slots / a.Hkv;
-      int32_t end = 0;
-      for (int again = 0; again < 2; ++again) {
-        p0 = cut(b0), p1 = cut(b1);
-        end = scan(c0 * p0 + c1 * p1);
-        // a few parts more than CTAs would take a second turn: rather longer parts
-        const int64_t all = static_cast<int64_t>(__shfl_sync(0xffffffffu, end, 31)) * a.Hkv;
-        if (all <= gridDim.x || 20 * all > 27ll * gridDim.x) break;
-        length = static_cast<int32_t>((static_cast<int64_t>(length) * all + gridDim.x - 1) / gridDim.x);
+        auto cut = [&](int b) -> int32_t {
+          const int64_t most = (((static_cast<int64_t>(b + 1) << bucket) + 1) << unit_shift) / kPaKeys + 1,
+                        least = ((static_cast<int64_t>(b) << bucket) << unit_shift) / kPaKeys;
+          // a unit a little over the share is better left whole; a bucket of short ones beside a long one too
+          if (10 * most <= 13ll * length || most < length + kPaMinSave || 2 * least < length) return 1;
+          const float n = ceilf(static_cast<float>(most) / static_cast<float>(length));
+          return n < kPaMaxParts ? static_cast<int32_t>(n) : kPaMaxParts;
+        };
+        const int32_t room = a.slots / a.Hkv;
+        int32_t end = 0;
+        for (int again = 0; again < 2; ++again) {
+          p0 = cut(b0), p1 = cut(b1);
+          end = scan(c0 * p0 + c1 * p1);
+          // a few parts more than CTAs would take a second turn: rather longer parts
+          const int64_t all = static_cast<int64_t>(__shfl_sync(0xffffffffu, end, 31)) * a.Hkv;
+          if (all <= gridDim.x || 20 * all > 27ll * gridDim.x) break;
+          length = static_cast<int32_t>((static_cast<int64_t>(length) * all + gridDim.x - 1) / gridDim.x);
+        }
+        if (end - c1 * p1 > room) p0 = 1;
+        if (end > room) p1 = 1;
       }
-      if (end - c1 * p1 > room) p0 = 1;
-      if (end > room) p1 = 1;
-    }
-    const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
+      const int32_t n0 = c0 * p0, n1 = c1 * p1, upto = scan(n0 + n1);
       sh.parts[b0] = p0;
       sh.parts[b1] = p1;
       sh.count[b0] = n0;
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
               n = to > from ? to - from : 0;
             }
             int32_t inc = n;
-  #pragma unroll
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
               const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
               if (lane >= o) inc += y;
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             for (int pl = 0; pl < L::kPlanes; ++pl)
               if (t == 0 || !a.single)
                 tma_load_4d(smem_u32(smem) + t * L::kTile + pl * kPaPlane, &tm_q, bar(sh.bars.q_full), 64 * pl,
-                          x.kvh * a.group, x.q0 + t * tokens_per_tile, 0);
+                            x.kvh * a.group, x.q0 + t * tokens_per_tile, 0);
         }
         // K_0, V_0, K_1, V_1, ...
         if (!kPaged) {

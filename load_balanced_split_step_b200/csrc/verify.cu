@@ -13,9 +13,12 @@
 // from HBM. A warp owns a contiguous run of the vocabulary and sums it; the sums meet in distributed
 // shared memory; the CTA whose run holds the crossing reads it again (from L2) to find it.
 //
-// Bound by the row streams and, close behind, by the conversions to fp64 (one per value, 16 lanes per cycle and
-// SM). 64 requests, vocabulary 131071, fp32: 16.8 us with the launch, 4.0 TB/s; 25 us with every value tested
-// in fp64, 39 us with one warp searching the run. One request of 32000: 6.4 us, latencies.
+// A call is about 5 us of latencies (launch, the drafts' words, two passes; one request of 32000 takes no more) and the row
+// streams. 64 requests, vocabulary 131071, fp32: 11.9 us where every draft is kept and one row read, 18.6 where every one is
+// rejected and two are (the second at 4.8 TB/s), 16.4 mixed: the requests with two rows set the time, with as many CTAs
+// each as those with one. (25 us with every value tested in fp64, 39 us with one warp searching the run; the
+// conversions to fp64 are under 4 us of it.) bf16 takes 14.5: half of the bytes in as many loads. A one-hot draft that is
+// rejected has every value tested, for the one that is left out: 23.6.
 #include <type_traits>
 
 #include "hpc_common.cuh"
