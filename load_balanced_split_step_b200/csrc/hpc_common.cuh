@@ -75,7 +75,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 // Let the next kernel on the stream launch now; it still waits in pdl_wait() for this one.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: bound on any pipeline wait
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: bound on any pipeline wait (prompt attention adds to it)
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -48,8 +48,8 @@
 // K, warp 10 those with V, warp 9 looks up units and loads, warp 11 checks V. A softmax thread holds the 128
 // scores of its row, so the softmax warpgroups take registers from the third (208 + 208 + 88 = 3 x the 168 of the
 // launch). Every wait is bounded and ends in HPC_DEV_TIMEOUT: by 2 s and 64 us for each key that a sequence can have,
-// since rows that are done one by one (values that are not finite) keep the other roles waiting. 32 rows of a warp took
-// 0.19 to 0.65 us for each key (packed, and pages of 16 with every CTA at it), so that 2 s alone passed at 96000 keys.
+// since rows that are done one by one (values that are not finite) keep the other roles waiting. The 32 rows of a warp
+// took 6 to 21 us for each key (packed, and pages of 16 with every CTA at it), so that 2 s alone passed at 96000 keys.
 // (Waits that look whether such rows advance kept to 2 s, and cost 2 to 12% of every call.)
 #include <cmath>
 
